@@ -33,7 +33,8 @@
  *     (nothing is launched then) or from the CUDA launch itself.  Faults found
  *     on the device (a sequence length past the capacity) never trap: they are
  *     written to a status word and the offending length is clamped.
- *   - Every device pointer must be 16-byte aligned.
+ *   - Every device pointer must be 16-byte aligned (4-byte where a call says
+ *     so, and the page tables, lengths, counts and lists of the paged cache).
  */
 #ifndef MAGICPIG_H
 #define MAGICPIG_H
@@ -291,6 +292,199 @@ int mp_decode_attend_q8(const mp_shape *shape, const void *q, const void *W, con
                         const int8_t *k8, const void *v_cache, const int32_t *seq_lens, int32_t max_len,
                         float *out, float *lse, int32_t *n_sampled, void *workspace, size_t workspace_bytes,
                         const mp_decode_debug *debug, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Exact attention: prompts, and decode over a paged key-value cache.
+ *
+ * The sampled decode above needs a cache that something filled, and a model
+ * keeps some layers (and short sequences) exact.  These calls are the exact
+ * counterparts: causal attention over the prompts of a batch, the append of
+ * new key and value rows into the pages of a cache, one decode step over such
+ * a cache, and the operations on its pages.  With scale = 1 / sqrt(head_dim),
+ * natural logarithms:
+ *   out_i = sum_j exp(scale q_i . k_j) v_j / sum_j exp(scale q_i . k_j),
+ *   lse_i = log sum_j exp(scale q_i . k_j),
+ * over the keys j that query i sees.  A query that sees no key gets out = 0
+ * and lse = -inf.  Heads are grouped as everywhere (query head h reads kv head
+ * h / G, G = n_q_heads / n_kv_heads); any G from 1 to 8 is supported.
+ * Products are bf16 tensor-core products with fp32 accumulation; maxima, sums
+ * and lse are fp32.
+ *
+ * Each `status` below is a nullable int32 device word, 4-byte aligned, that
+ * is written only when the call finds something wrong on the device (so the
+ * caller clears it); the first error stays.
+ */
+
+/*
+ * Shape of mp_prompt_attend.  Supported: batch >= 1; head_dim == 128;
+ * G in 1 .. 8; 0 <= total < 2^28; strides in elements, multiples of 8 (16
+ * bytes), at least n_heads * head_dim.
+ */
+typedef struct mp_prompt_shape {
+    int32_t batch;      /* B: sequences in the batch */
+    int32_t n_q_heads;  /* Hq */
+    int32_t n_kv_heads; /* Hkv */
+    int32_t head_dim;   /* d */
+    int32_t total;      /* T: token rows of q, k, v, out and lse */
+    int32_t q_stride;   /* elements from one token's row of q to the next (0: n_q_heads * head_dim) */
+    int32_t k_stride;   /* the same of k (0: n_kv_heads * head_dim) */
+    int32_t v_stride;   /* the same of v (0: n_kv_heads * head_dim) */
+} mp_prompt_shape;
+
+/*
+ * Causal attention over whole prompts of different lengths, packed one after
+ * another: sequence b is rows [cu_lens[b], cu_lens[b + 1]) and its token i
+ * sees tokens 0 .. i of the same sequence.
+ *   q  bf16 [T][Hq][d], k and v bf16 [T][Hkv][d], the heads of a token side
+ *      by side, tokens q_stride / k_stride / v_stride elements apart (so the
+ *      three may be parts of one fused projection's rows)
+ *   cu_lens  int32 [B + 1] device, 4-byte aligned, not decreasing, from >= 0
+ *      to <= T.  A sequence whose two entries break that is skipped and
+ *      MP_ERR_CAPACITY recorded.
+ *   out  bf16 [T][Hq][d]     lse  fp32 [T][Hq] (nullable)
+ * Rows of no sequence (behind the last one, say) are neither used nor
+ * written; what they hold in q, k and v, NaN included, has no effect.  Within
+ * a sequence the values v must be finite: a value that is not reaches the
+ * rows before it that share a tile with it.
+ * A weight exp(.) is rounded to bf16 before it multiplies its v (relative
+ * 2^-9, about the rounding of out itself); lse comes from the unrounded fp32.
+ * status also receives MP_ERR_CUDA if the kernel's internal pipeline stalled
+ * (a bounded wait expired; out and lse are then incomplete).
+ */
+int mp_prompt_attend(const mp_prompt_shape *shape, const void *q, const void *k, const void *v,
+                     const int32_t *cu_lens, void *out, float *lse, int32_t *status, void *stream);
+
+/*
+ * Shape of a paged key-value cache.  Supported: 1 <= batch <= 4096;
+ * head_dim == 128; G in 1 .. 8; 1 <= n_pages <= 2^24; 1 <= page_size < 2^24;
+ * max_pages >= 1; max_pages * page_size < 2^30; batch * n_kv_heads <= 65535.
+ */
+typedef struct mp_pages_shape {
+    int32_t batch;      /* B: sequences (rows of the page table) */
+    int32_t n_q_heads;  /* Hq */
+    int32_t n_kv_heads; /* Hkv */
+    int32_t head_dim;   /* d */
+    int32_t n_pages;    /* P: pages of the pools */
+    int32_t page_size;  /* S: tokens a page */
+    int32_t max_pages;  /* M: columns of the page table */
+} mp_pages_shape;
+
+/*
+ * A paged cache, all of it the caller's:
+ *   k_pages, v_pages  bf16 [P][Hkv][S][d]: the pools of one layer
+ *   page_table  int32 [B][M]: the pages of a sequence in order, then -1
+ *   seq_lens    int32 [B]: tokens of a sequence; token i is row i % S of page
+ *               page_table[b][i / S]
+ *   refs        int32 [P]: how many sequences hold a page; 0 means free
+ * A table, its lengths and its counts serve every layer of a model (one pair
+ * of pools a layer).  Start: table all -1, lengths and counts 0.  The
+ * contiguous cache of mp_append_token is the case S = Ncap, M = 1, P = B with
+ * page_table[b][0] = b, so mp_paged_attend also reads that one.
+ */
+
+/* Workspace bytes that mp_paged_attend needs for sequences up to max_len. */
+int mp_paged_workspace_bytes(const mp_pages_shape *shape, int32_t max_len, size_t *bytes);
+
+/*
+ * One exact decode step: the one new query of every sequence over all tokens
+ * that its pages hold.
+ *   q  bf16 [B][Hq][d]
+ *   max_len  host bound on every seq_lens[b], 0 <= max_len <= M * S (sizes the
+ *            grid); a longer sequence is cut there, MP_ERR_CAPACITY recorded
+ *   out  fp32 [B][Hq][d]     lse  fp32 [B][Hq]
+ *   workspace  device scratch of at least mp_paged_workspace_bytes bytes (16
+ *            where that is 0); its contents need not be kept or cleared.  Two
+ *            calls that may run at the same time need one each.
+ * Rows of a page past the sequence's length may hold anything.  A page number
+ * outside [0, P) within a sequence's length: its tokens are left out and
+ * MP_ERR_CAPACITY recorded.  Weights keep 24 bits (three bf16 parts) in their
+ * product with v.
+ */
+int mp_paged_attend(const mp_pages_shape *shape, const void *q, const void *k_pages, const void *v_pages,
+                    const int32_t *page_table, const int32_t *seq_lens, int32_t max_len, float *out, float *lse,
+                    void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * Writes new key and value rows behind the tokens that the sequences hold:
+ * row r of sequence b goes to its position seq_lens[b] + r.
+ *   k_new, v_new  bf16 [n_rows][Hkv][d], tokens k_stride / v_stride elements
+ *            apart (0: n_kv_heads * head_dim; else multiples of 8, at least that)
+ *   cu_new   int32 [B + 1] device: sequence b has rows [cu_new[b], cu_new[b + 1]);
+ *            null: one row for each sequence (n_rows == batch).  Entries as for
+ *            cu_lens of mp_prompt_attend, up to n_rows.
+ *   advance  nonzero: seq_lens[b] grows by the sequence's rows.  Zero: the
+ *            lengths stay (all layers of a model but the last, which share them).
+ * The pages must be there (mp_pages_reserve) and no other sequence may hold
+ * the ones written to.  A row whose page is missing or outside [0, P) is not
+ * written, MP_ERR_CAPACITY is recorded, and the length of its sequence stays.
+ */
+int mp_paged_append(const mp_pages_shape *shape, const void *k_new, const void *v_new, int32_t k_stride,
+                    int32_t v_stride, const int32_t *cu_new, int32_t n_rows, int32_t advance,
+                    const int32_t *page_table, int32_t *seq_lens, void *k_pages, void *v_pages, int32_t *status,
+                    void *stream);
+
+/*
+ * Takes free pages so that every sequence b can hold seq_lens[b] + n_new[b]
+ * tokens (n_new[b] <= 0: nothing).  The lowest-numbered free pages are taken,
+ * in the order of (sequence, position); each gets a count of 1.  If there are
+ * too few, or a row of the table too short, nothing is taken and
+ * MP_ERR_CAPACITY is recorded.
+ */
+int mp_pages_reserve(const mp_pages_shape *shape, const int32_t *n_new, int32_t *page_table,
+                     const int32_t *seq_lens, int32_t *refs, int32_t *status, void *stream);
+
+/*
+ * Makes sequence dst[i] a copy of sequence src[i], i = 0 .. n - 1 (one source
+ * may be named often).  Full pages are shared (their count grows); a partly
+ * filled last page is not: dst gets a free page of its own for it (the lowest
+ * ones, in the order of the list), and `copies` says what has to be copied
+ * there, by mp_pages_copy on every layer's pools.  Pages that src holds past
+ * its length are not shared.
+ *   src, dst  int32 [n] device; 1 <= n <= B
+ *   copies    int32 [1 + n][4] device, 16-byte aligned, written
+ * Refused as a whole (nothing changes, copies is written as an empty list): a
+ * number outside [0, B), a dst that holds pages, that is named twice or that
+ * is also a source, a src whose table does not cover its length, or a count
+ * below 1 on one of its pages (MP_ERR_ARG); too few free pages
+ * (MP_ERR_CAPACITY).
+ */
+int mp_pages_fork(const mp_pages_shape *shape, const int32_t *src, const int32_t *dst, int32_t n,
+                  int32_t *page_table, int32_t *seq_lens, int32_t *refs, int32_t *copies, int32_t *status,
+                  void *stream);
+
+/*
+ * Ends sequences seqs[i], i = 0 .. n - 1: every page of theirs loses one
+ * count, their table rows become -1 and their lengths 0.  A sequence that
+ * holds nothing, or that the list names again, is left as it is.
+ *   seqs  int32 [n] device; 1 <= n <= B.  A number outside [0, B), or a page
+ *         whose count is 0 already, is skipped and MP_ERR_ARG recorded.
+ */
+int mp_pages_free(const mp_pages_shape *shape, const int32_t *seqs, int32_t n, int32_t *page_table,
+                  int32_t *seq_lens, int32_t *refs, int32_t *status, void *stream);
+
+/*
+ * Brings the pages in use together: with U pages in use, they become pages
+ * 0 .. U - 1.  The i-th page in use at or past U moves to the i-th free page
+ * below U, the others stay; table and counts follow, and `copies` says what
+ * has to be copied, by mp_pages_copy on every layer's pools.
+ *   copies  int32 [1 + P / 2][4] device, 16-byte aligned, written
+ */
+int mp_pages_compact(const mp_pages_shape *shape, int32_t *page_table, int32_t *refs, int32_t *copies,
+                     int32_t *status, void *stream);
+
+/*
+ * Copies pages within one layer's pools.
+ *   copies  int32 [1 + n][4] device, 16-byte aligned: entry 0 is {count, 0, 0,
+ *           0}, entries 1 .. count are {src page, dst page, rows, 0}: the
+ *           first `rows` rows of every head, keys and values.  From
+ *           mp_pages_fork, mp_pages_compact or the caller.
+ *   max_copies  host bound n on the count
+ * No page may be a destination twice, or a source and a destination.  An
+ * entry with a page outside [0, P) or rows outside [0, S] is skipped, a count
+ * outside [0, n] is cut, and MP_ERR_ARG recorded.
+ */
+int mp_pages_copy(const mp_pages_shape *shape, const int32_t *copies, int32_t max_copies, void *k_pages,
+                  void *v_pages, int32_t *status, void *stream);
 
 /* Synchronises `stream` and reads the status word of a decode workspace. */
 int mp_read_status(const void *workspace, int32_t *status, void *stream);

@@ -8,6 +8,8 @@ raises.
 """
 from ._binding import (  # noqa: F401
     MagicPIGError,
+    PagesShape,
+    PromptShape,
     Shape,
     append_token,
     append_token_q8,
@@ -23,6 +25,15 @@ from ._binding import (  # noqa: F401
     hash_queries,
     library,
     library_path,
+    paged_append,
+    paged_attend,
+    paged_workspace_bytes,
+    pages_compact,
+    pages_copy,
+    pages_fork,
+    pages_free,
+    pages_reserve,
+    prompt_attend,
     quantize_keys,
     read_status,
     status_string,
@@ -49,5 +60,6 @@ __all__ = [
     "MagicPIGError", "Shape", "append_token", "append_token_q8", "auto_planes", "codes_bytes", "codes_shape", "decode_attend",
     "decode_attend_noalloc", "decode_attend_q8", "quantize_keys",
     "decode_workspace_bytes", "hash_keys", "hash_keys_range", "hash_queries", "library", "library_path", "read_status",
-    "status_string",
+    "status_string", "PagesShape", "PromptShape", "paged_append", "paged_attend", "paged_workspace_bytes",
+    "pages_compact", "pages_copy", "pages_fork", "pages_free", "pages_reserve", "prompt_attend",
 ]

@@ -8,6 +8,7 @@
 #include "magicpig.h"
 #include "mp_common.cuh"
 #include "mp_kernels.cuh"
+#include "mp_pages.cuh"
 
 namespace mp {
 
@@ -46,6 +47,58 @@ int validate_shape(const mp_shape *in, Shape &s)
     return MP_OK;
 }
 
+// Heads of the exact-attention shapes: head_dim 128, groups of 1 to 8.
+static int validate_heads(int n_q, int n_kv, int d, int &G)
+{
+    if (n_q < 1 || n_kv < 1 || d != kHeadDim || n_q % n_kv != 0) return MP_ERR_SHAPE;
+    G = n_q / n_kv;
+    return G <= kMaxGroup ? MP_OK : MP_ERR_SHAPE;
+}
+
+// A token stride in elements (0: the heads side by side).
+static int token_stride(int32_t given, int heads, int64_t &out)
+{
+    out = given == 0 ? (int64_t)heads * kHeadDim : given;
+    if (given != 0 && (given < (int64_t)heads * kHeadDim || given % 8 != 0)) return MP_ERR_SHAPE;
+    return MP_OK;
+}
+
+int validate_prompt_shape(const mp_prompt_shape *in, PromptShape &s)
+{
+    if (!in) return MP_ERR_ARG;
+    s.B = in->batch;
+    s.Hq = in->n_q_heads;
+    s.Hkv = in->n_kv_heads;
+    s.T = in->total;
+    int r = validate_heads(s.Hq, s.Hkv, in->head_dim, s.G);
+    if (r) return r;
+    if (s.Hq > 65535) return MP_ERR_SHAPE;
+    if (s.B < 1 || s.T < 0 || s.T >= (1 << 28)) return MP_ERR_SHAPE;
+    if ((r = token_stride(in->q_stride, s.Hq, s.qs)) || (r = token_stride(in->k_stride, s.Hkv, s.ks)) ||
+        (r = token_stride(in->v_stride, s.Hkv, s.vs)))
+        return r;
+    // items of the largest group (16 tokens a query tile) have to fit the grid
+    if (((int64_t)s.T / (2 * (128 / s.G)) + s.B) * s.Hkv > 0x7fffffff) return MP_ERR_SHAPE;
+    return MP_OK;
+}
+
+int validate_pages_shape(const mp_pages_shape *in, PagesShape &s)
+{
+    if (!in) return MP_ERR_ARG;
+    s.B = in->batch;
+    s.Hq = in->n_q_heads;
+    s.Hkv = in->n_kv_heads;
+    s.P = in->n_pages;
+    s.S = in->page_size;
+    s.M = in->max_pages;
+    int r = validate_heads(s.Hq, s.Hkv, in->head_dim, s.G);
+    if (r) return r;
+    if (s.B < 1 || s.B > kPagesMaxBatch || s.P < 1 || s.P > (1 << 24) || s.S < 1 || s.S >= (1 << 24) || s.M < 1)
+        return MP_ERR_SHAPE;
+    if ((int64_t)s.M * s.S >= (1 << 30) || (int64_t)s.B * s.Hkv > 65535) return MP_ERR_SHAPE;
+    return MP_OK;
+}
+
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_ptrs(std::initializer_list<const void *> ptrs)
@@ -53,6 +106,18 @@ int check_ptrs(std::initializer_list<const void *> ptrs)
     for (const void *p : ptrs) {
         if (!p) return MP_ERR_ARG;
         if (!aligned16(p)) return MP_ERR_ALIGN;
+    }
+    return MP_OK;
+}
+
+static bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Tables, counts and lists of 32-bit words.
+static int check_words(std::initializer_list<const void *> ptrs)
+{
+    for (const void *p : ptrs) {
+        if (!p) return MP_ERR_ARG;
+        if (!aligned4(p)) return MP_ERR_ALIGN;
     }
     return MP_OK;
 }
@@ -235,6 +300,132 @@ int mp_decode_attend_q8(const mp_shape *shape, const void *q, const void *W, con
     return cuda_status(launch_decode(s, static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(W), codes,
                                      nullptr, static_cast<const uint16_t *>(v_cache), seq_lens, max_len, out, lse,
                                      n_sampled, workspace, debug, static_cast<cudaStream_t>(stream), k8));
+}
+
+int mp_prompt_attend(const mp_prompt_shape *shape, const void *q, const void *k, const void *v,
+                     const int32_t *cu_lens, void *out, float *lse, int32_t *status, void *stream)
+{
+    PromptShape s;
+    int r = validate_prompt_shape(shape, s);
+    if (r) return r;
+    if ((r = check_words({cu_lens}))) return r;
+    if (s.T == 0) return MP_OK;
+    if ((r = check_ptrs({q, k, v, out}))) return r;
+    if (!aligned4(lse) || !aligned4(status)) return MP_ERR_ALIGN;
+    return cuda_status(launch_prompt(s, static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k),
+                                     static_cast<const uint16_t *>(v), cu_lens, static_cast<uint16_t *>(out), lse, status,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+int mp_paged_workspace_bytes(const mp_pages_shape *shape, int32_t max_len, size_t *bytes)
+{
+    PagesShape s;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if (!bytes) return MP_ERR_ARG;
+    if (max_len < 0 || max_len > (int64_t)s.M * s.S) return MP_ERR_CAPACITY;
+    *bytes = paged_workspace_bytes(s, max_len);
+    return MP_OK;
+}
+
+int mp_paged_attend(const mp_pages_shape *shape, const void *q, const void *k_pages, const void *v_pages,
+                    const int32_t *page_table, const int32_t *seq_lens, int32_t max_len, float *out, float *lse,
+                    void *workspace, size_t workspace_bytes, int32_t *status, void *stream)
+{
+    PagesShape s;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if ((r = check_ptrs({q, k_pages, v_pages, out, workspace})) || (r = check_words({page_table, seq_lens, lse}))) return r;
+    if (!aligned4(status)) return MP_ERR_ALIGN;
+    if (max_len < 0 || max_len > (int64_t)s.M * s.S) return MP_ERR_CAPACITY;
+    if (workspace_bytes < paged_workspace_bytes(s, max_len)) return MP_ERR_WORKSPACE;
+    return cuda_status(launch_paged_attend(s, static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k_pages),
+                                           static_cast<const uint16_t *>(v_pages), page_table, seq_lens, max_len, out, lse,
+                                           workspace, status, static_cast<cudaStream_t>(stream)));
+}
+
+int mp_paged_append(const mp_pages_shape *shape, const void *k_new, const void *v_new, int32_t k_stride,
+                    int32_t v_stride, const int32_t *cu_new, int32_t n_rows, int32_t advance,
+                    const int32_t *page_table, int32_t *seq_lens, void *k_pages, void *v_pages, int32_t *status,
+                    void *stream)
+{
+    PagesShape s;
+    int64_t ks, vs;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if ((r = token_stride(k_stride, s.Hkv, ks)) || (r = token_stride(v_stride, s.Hkv, vs))) return r;
+    if (n_rows < 0 || n_rows >= (1 << 28) || (!cu_new && n_rows != s.B)) return MP_ERR_ARG;
+    if (n_rows == 0) return MP_OK;
+    if ((r = check_ptrs({k_new, v_new, k_pages, v_pages})) || (r = check_words({page_table, seq_lens}))) return r;
+    if (!aligned4(cu_new) || !aligned4(status)) return MP_ERR_ALIGN;
+    return cuda_status(launch_paged_append(s, static_cast<const uint16_t *>(k_new), static_cast<const uint16_t *>(v_new),
+                                           ks, vs, cu_new, n_rows, advance, page_table, seq_lens,
+                                           static_cast<uint16_t *>(k_pages), static_cast<uint16_t *>(v_pages), status,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+int mp_pages_reserve(const mp_pages_shape *shape, const int32_t *n_new, int32_t *page_table, const int32_t *seq_lens,
+                     int32_t *refs, int32_t *status, void *stream)
+{
+    PagesShape s;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if ((r = check_words({n_new, page_table, seq_lens, refs}))) return r;
+    if (!aligned4(status)) return MP_ERR_ALIGN;
+    return cuda_status(launch_pages_reserve(s, n_new, page_table, seq_lens, refs, status,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int mp_pages_fork(const mp_pages_shape *shape, const int32_t *src, const int32_t *dst, int32_t n,
+                  int32_t *page_table, int32_t *seq_lens, int32_t *refs, int32_t *copies, int32_t *status,
+                  void *stream)
+{
+    PagesShape s;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if ((r = check_ptrs({copies})) || (r = check_words({src, dst, page_table, seq_lens, refs}))) return r;
+    if (!aligned4(status)) return MP_ERR_ALIGN;
+    if (n < 1 || n > s.B) return MP_ERR_ARG;
+    return cuda_status(launch_pages_fork(s, src, dst, n, page_table, seq_lens, refs, copies, status,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int mp_pages_free(const mp_pages_shape *shape, const int32_t *seqs, int32_t n, int32_t *page_table,
+                  int32_t *seq_lens, int32_t *refs, int32_t *status, void *stream)
+{
+    PagesShape s;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if ((r = check_words({seqs, page_table, seq_lens, refs}))) return r;
+    if (!aligned4(status)) return MP_ERR_ALIGN;
+    if (n < 1 || n > s.B) return MP_ERR_ARG;
+    return cuda_status(launch_pages_free(s, seqs, n, page_table, seq_lens, refs, status,
+                                         static_cast<cudaStream_t>(stream)));
+}
+
+int mp_pages_compact(const mp_pages_shape *shape, int32_t *page_table, int32_t *refs, int32_t *copies,
+                     int32_t *status, void *stream)
+{
+    PagesShape s;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if ((r = check_ptrs({copies})) || (r = check_words({page_table, refs}))) return r;
+    if (!aligned4(status)) return MP_ERR_ALIGN;
+    return cuda_status(launch_pages_compact(s, page_table, refs, copies, status, static_cast<cudaStream_t>(stream)));
+}
+
+int mp_pages_copy(const mp_pages_shape *shape, const int32_t *copies, int32_t max_copies, void *k_pages,
+                  void *v_pages, int32_t *status, void *stream)
+{
+    PagesShape s;
+    int r = validate_pages_shape(shape, s);
+    if (r) return r;
+    if ((r = check_ptrs({copies, k_pages, v_pages}))) return r;
+    if (!aligned4(status)) return MP_ERR_ALIGN;
+    if (max_copies < 0) return MP_ERR_ARG;
+    if (max_copies == 0) return MP_OK;
+    return cuda_status(launch_pages_copy(s, copies, max_copies, static_cast<uint16_t *>(k_pages),
+                                         static_cast<uint16_t *>(v_pages), status, static_cast<cudaStream_t>(stream)));
 }
 
 int mp_read_status(const void *workspace, int32_t *status, void *stream)

@@ -1,0 +1,425 @@
+// Exact decode attention over a paged key-value cache (mp_paged_attend).
+//
+// For each unit (sequence b, kv head) and the G query heads of its group:
+//   s_ih = q_h . k_i / sqrt(d),  out_h = sum_i e^{s_ih} v_i / sum_i e^{s_ih},
+// one pass over the unit's tokens with a running maximum and sum per head.
+// The floor is HBM: 512 bytes per (token, kv head), each read once; the
+// products are 2 d G multiply-adds on them, far below the tensor rate.
+//
+// Split: the 64-token blocks of all units, unit after unit, form one line of
+// W blocks, and the C thread blocks of the grid (two per SM) take equal runs
+// of it, c W / C to (c + 1) W / C.  So every thread block reads the same
+// number of bytes whatever the lengths are, one long sequence is split over
+// all SMs and a batch of short ones hardly at all.  A run that covers a whole
+// unit writes its result; a unit cut by the ends of runs leaves one partial
+// (m, l, acc) per run, at most two per thread block, and merge_partials_kernel
+// joins them.
+//
+// Within a thread block, warp w takes the 16-token tiles 4 j + w of a run,
+// each warp on its own: its rows come through its own ring of cp.async copies
+// (kStages tiles of 16 K and 16 V rows), S^T = K Q^T and O^T += V^T P^T run on
+// mma.sync m16n8k16 (tokens or dims x 8 heads x 16), the softmax state stays
+// in registers, and the warps meet only at the end of a unit.  mma.sync and
+// not tcgen05: 8 heads fill a 16-row tile of either poorly, and the tensor
+// pipe idles here anyway.  P enters its product as three bf16 parts (24 bits):
+// the result is fp32, and one bf16 part would cost 2^-9.
+#include <math.h>
+
+#include "mp_pages.cuh"
+
+namespace mp {
+namespace paged {
+
+constexpr int kWarps = 4;
+constexpr int kTile = 16;                    // tokens of a warp's tile
+constexpr int kBlockTok = kWarps * kTile;    // tokens of a block of the split
+constexpr int kStages = 3;
+constexpr int kRowBytes = 256;
+constexpr int kTileBytes = 2 * kTile * kRowBytes;        // K rows, then V rows
+constexpr int kRingBytes = kWarps * kStages * kTileBytes; // 96 KB: two thread blocks per SM
+constexpr int kBlocksPerSm = 2;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMargin = 8.f;               // log2 units that a maximum may grow before the sums are rescaled
+
+struct Args {
+    PagesShape s;
+    const uint16_t *q, *kp, *vp;
+    const int32_t *table, *lens;
+    int max_len, C;
+    float *out, *lse;
+    float *pml;   // [C][2][8][2]: m, l (log2 units) of the partials
+    float *pacc;  // [C][2][8][128]
+    int32_t *status;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// {lo, hi} as two bf16
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ void ldmatrix_x4_s(uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3, uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans_s(uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3, uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                 : "r"(addr)
+                 : "memory");
+}
+// Byte offset of 16-byte piece c (0..15) of a 256-byte row in a tile: pieces
+// XOR-swizzled by the row within each 128-byte line, so the 8 rows that one
+// ldmatrix phase reads hit distinct banks.
+__device__ __forceinline__ uint32_t row_off(int r, int c) { return (uint32_t)(r * kRowBytes + ((c ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ int clamped_len(const Args &a, int b)
+{
+    return min(max(a.lens[b], 0), a.max_len);
+}
+__device__ __forceinline__ int blocks_of(int len) { return (len + kBlockTok - 1) / kBlockTok; }
+
+// Sum over the sequences of their 64-token blocks; with `upto` given, only
+// those before it.
+__device__ __forceinline__ long long blocks_before(const Args &a, int upto, int lane)
+{
+    long long n = 0;
+    for (int b = lane; b < upto; b += 32) n += blocks_of(clamped_len(a, b));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// Runs that the line is cut into: C, or W where that is less (so no run is
+// empty).  The run that holds block x is the largest c with c W / C <= x.
+__device__ __forceinline__ int live_runs(long long W, int C) { return (int)min(W, (long long)C); }
+__device__ __forceinline__ int run_of(long long x, long long W, int C) { return (int)(((x + 1) * C - 1) / W); }
+
+__global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel(const Args a)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ uint32_t seen_sh[kWarps][kStages];  // bit i: token i of the stage's tile counts
+    __shared__ float red_ml[kWarps][2][8];
+    const PagesShape &s = a.s;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g4 = lane >> 2, t4 = lane & 3;  // mma fragment row and column group
+    const int h0 = 2 * t4, h1 = h0 + 1;       // this lane's heads of the group
+    const float scale2 = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
+    grid_dependency_wait();
+
+    // this thread block's run of the line
+    const long long seq_blocks = blocks_before(a, s.B, lane);
+    const long long W = seq_blocks * s.Hkv;
+    const int c = blockIdx.x, C = live_runs(W, a.C);
+    if (c == 0)
+        for (int j = tid; j < s.B; j += blockDim.x)
+            if (a.lens[j] > a.max_len || a.lens[j] < 0) set_status(a.status, MP_ERR_CAPACITY);
+    if (c >= C) return;
+    long long x = c * W / C;
+    const long long x_end = (c + 1) * W / C;
+    // the sequence that x falls into: 32 sequences a step
+    int b = 0;
+    long long first = 0;  // the line's position of sequence b
+    for (int b0 = 0;; b0 += 32) {
+        const int bb = b0 + lane;
+        const long long n = bb < s.B ? (long long)blocks_of(clamped_len(a, bb)) * s.Hkv : 0;
+        long long pre = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+            if (lane >= o) pre += y;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, first + pre > x);
+        if (over) {
+            const int l = __ffs((int)over) - 1;
+            b = b0 + l;
+            first += __shfl_sync(0xffffffffu, pre - n, l);
+            break;
+        }
+        first += __shfl_sync(0xffffffffu, pre, 31);
+    }
+
+    const uint32_t my_ring = smem_u32(ring) + (uint32_t)(warp * kStages * kTileBytes);
+    while (x < x_end) {
+        const int len = clamped_len(a, b), nb = blocks_of(len);
+        if (nb == 0) {
+            b++;
+            continue;
+        }
+        const int kvh = (int)((x - first) / nb);
+        const int blk0 = (int)((x - first) % nb);
+        const int blk1 = (int)min((long long)nb, blk0 + (x_end - x));
+        const int32_t *row = a.table + (size_t)b * s.M;
+        const int hq0 = kvh * s.G;
+
+        // query fragments: B of m16n8k16 (k = dims, n = heads), zero for heads past G
+        uint32_t qf[8][2];
+#pragma unroll
+        for (int ks = 0; ks < 8; ks++)
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const uint16_t *qr = a.q + ((size_t)b * s.Hq + hq0 + g4) * kHeadDim + ks * 16 + j * 8 + t4 * 2;
+                qf[ks][j] = g4 < s.G ? *reinterpret_cast<const uint32_t *>(qr) : 0u;
+            }
+
+        // tiles of this warp: tokens (blk0 * 4 + warp + 4 t) * 16
+        const int nt = blk1 - blk0;
+        auto issue = [&](int t) {
+            if (t < nt) {
+                const int tok0 = ((blk0 + t) * kWarps + warp) * kTile;
+                const uint32_t dst = my_ring + (uint32_t)((t % kStages) * kTileBytes);
+                // lanes 0..15: the row of token tok0 + lane in the pools (-1: none)
+                long long at = -1;
+                const int tok = tok0 + (lane & 15);
+                if (tok < len) {
+                    const int page = row[tok / s.S];
+                    if (page >= 0 && page < s.P) at = ((long long)page * s.Hkv + kvh) * s.S + tok % s.S;
+                    else set_status(a.status, MP_ERR_CAPACITY);
+                }
+                const unsigned seen = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int r = 2 * i + (lane >> 4), p = lane & 15;
+                    const long long ar = __shfl_sync(0xffffffffu, at, r);
+                    const size_t off = (size_t)max(ar, 0ll) * kHeadDim + p * 8;
+                    const int n = ar >= 0 ? 16 : 0;  // a row that does not count is zeros: 0 times anything else may be NaN
+                    cp_async_16_s(dst + row_off(r, p), a.kp + off, n);
+                    cp_async_16_s(dst + kTile * kRowBytes + row_off(r, p), a.vp + off, n);
+                }
+                if (lane == 0) seen_sh[warp][t % kStages] = seen;
+            }
+            cp_async_commit();
+        };
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        float o[8][4];
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+#pragma unroll
+            for (int j = 0; j < 4; j++) o[i][j] = 0.f;
+        for (int t = 0; t < kStages - 1; t++) issue(t);
+        for (int t = 0; t < nt; t++) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            const uint32_t kt = my_ring + (uint32_t)((t % kStages) * kTileBytes), vt = kt + kTile * kRowBytes;
+            const unsigned seen = seen_sh[warp][t % kStages];
+            // S^T: 16 tokens x 8 heads
+            float c0 = 0.f, c1 = 0.f, c2 = 0.f, c3 = 0.f;
+#pragma unroll
+            for (int ks = 0; ks < 8; ks++) {
+                uint32_t r0, r1, r2, r3;
+                ldmatrix_x4_s(r0, r1, r2, r3, kt + row_off(lane & 15, 2 * ks + (lane >> 4)));
+                mma_bf16_16816(c0, c1, c2, c3, r0, r1, r2, r3, qf[ks][0], qf[ks][1]);
+            }
+            const bool s0 = (seen >> g4) & 1u, s1 = (seen >> (g4 + 8)) & 1u;
+            c0 = s0 ? c0 * scale2 : -INFINITY;
+            c1 = s0 ? c1 * scale2 : -INFINITY;
+            c2 = s1 ? c2 * scale2 : -INFINITY;
+            c3 = s1 ? c3 * scale2 : -INFINITY;
+            const float x0 = fmaxf(c0, c2), x1 = fmaxf(c1, c3);
+            if (__any_sync(0xffffffffu, x0 > m0 + kMargin || x1 > m1 + kMargin)) {
+                float y0 = x0, y1 = x1;
+#pragma unroll
+                for (int w = 4; w < 32; w <<= 1) {
+                    y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, w));
+                    y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, w));
+                }
+                y0 = fmaxf(y0, m0);
+                y1 = fmaxf(y1, m1);
+                const float f0 = m0 == -INFINITY ? 0.f : ex2(m0 - y0), f1 = m1 == -INFINITY ? 0.f : ex2(m1 - y1);
+                m0 = y0;
+                m1 = y1;
+                l0 *= f0;
+                l1 *= f1;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f1;
+                    o[i][2] *= f0;
+                    o[i][3] *= f1;
+                }
+            }
+            const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+            float p0 = ex2(c0 - u0), p1 = ex2(c1 - u1), p2 = ex2(c2 - u0), p3 = ex2(c3 - u1);
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            uint32_t pb[3][2];  // P^T as B fragments (k = tokens, n = heads), three bf16 parts
+#pragma unroll
+            for (int j = 0; j < 3; j++) {
+                const uint32_t a0 = pack_bf16(p0, p1), a1 = pack_bf16(p2, p3);
+                p0 -= bf16_lo(a0);
+                p1 -= bf16_hi(a0);
+                p2 -= bf16_lo(a1);
+                p3 -= bf16_hi(a1);
+                pb[j][0] = transpose8(a0);
+                pb[j][1] = transpose8(a1);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i++) {  // 16 dims each
+                uint32_t r0, r1, r2, r3;
+                ldmatrix_x4_trans_s(r0, r1, r2, r3, vt + row_off((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+                for (int j = 2; j >= 0; j--)
+                    mma_bf16_16816(o[i][0], o[i][1], o[i][2], o[i][3], r0, r1, r2, r3, pb[j][0], pb[j][1]);
+            }
+            __syncwarp();  // every lane has read the tile before its slot is refilled
+            issue(t + kStages - 1);
+        }
+        cp_async_wait<0>();
+        // ---- the warps' states, joined in the ring's memory ----
+#pragma unroll
+        for (int w = 4; w < 32; w <<= 1) {
+            l0 += __shfl_xor_sync(0xffffffffu, l0, w);
+            l1 += __shfl_xor_sync(0xffffffffu, l1, w);
+        }
+        __syncthreads();
+        float *acc_sh = reinterpret_cast<float *>(ring);  // [warp][8 heads][128 + 4]
+        constexpr int kPitch = kHeadDim + 4;
+        if (g4 == 0) {
+            red_ml[warp][0][h0] = m0;
+            red_ml[warp][0][h1] = m1;
+            red_ml[warp][1][h0] = l0;
+            red_ml[warp][1][h1] = l1;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            float *d0 = acc_sh + (warp * 8 + h0) * kPitch + i * 16 + g4;
+            float *d1 = acc_sh + (warp * 8 + h1) * kPitch + i * 16 + g4;
+            d0[0] = o[i][0];
+            d1[0] = o[i][1];
+            d0[8] = o[i][2];
+            d1[8] = o[i][3];
+        }
+        __syncthreads();
+        const bool whole = blk0 == 0 && blk1 == nb;
+        const int slot = c * 2 + (blk0 == 0 ? 1 : 0);
+        for (int h = 0; h < s.G; h++) {  // thread = dim
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) m = fmaxf(m, red_ml[w][0][h]);
+            float l = 0.f, v = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float f = red_ml[w][0][h] == -INFINITY ? 0.f : ex2(red_ml[w][0][h] - m);
+                l += f * red_ml[w][1][h];
+                v += f > 0.f ? f * acc_sh[(w * 8 + h) * kPitch + tid] : 0.f;
+            }
+            if (whole) {
+                const size_t bh = (size_t)b * s.Hq + hq0 + h;
+                a.out[bh * kHeadDim + tid] = l > 0.f ? v / l : (l == 0.f ? 0.f : v / l);
+                if (tid == 0) a.lse[bh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+            } else {
+                a.pacc[((size_t)slot * 8 + h) * kHeadDim + tid] = v;
+                if (tid == 0) {
+                    a.pml[((size_t)slot * 8 + h) * 2] = m;
+                    a.pml[((size_t)slot * 8 + h) * 2 + 1] = l;
+                }
+            }
+        }
+        __syncthreads();  // the ring is free again
+        x += blk1 - blk0;
+        if (kvh == s.Hkv - 1 && blk1 == nb) {
+            first += (long long)nb * s.Hkv;
+            b++;
+        }
+    }
+}
+
+// Joins the partials of the units that several runs share (block = unit,
+// thread = dim), and writes the units without tokens.
+__global__ void __launch_bounds__(kHeadDim) merge_partials_kernel(const Args a)
+{
+    const PagesShape &s = a.s;
+    const int unit = blockIdx.x, b = unit / s.Hkv, kvh = unit % s.Hkv, d = threadIdx.x, lane = d & 31;
+    // the lengths are older than this kernel's predecessor: read before the wait
+    const int nb = blocks_of(clamped_len(a, b));
+    const long long before = blocks_before(a, b, lane), W = blocks_before(a, s.B, lane) * s.Hkv;
+    const long long x0 = before * s.Hkv + (long long)kvh * nb;
+    grid_dependency_wait();
+    const size_t bh0 = (size_t)b * s.Hq + (size_t)kvh * s.G;
+    if (nb == 0) {
+        for (int h = 0; h < s.G; h++) {
+            a.out[(bh0 + h) * kHeadDim + d] = 0.f;
+            if (d == 0) a.lse[bh0 + h] = -INFINITY;
+        }
+        return;
+    }
+    const int C = live_runs(W, a.C), c0 = run_of(x0, W, C), c1 = run_of(x0 + nb - 1, W, C);
+    if (c0 == c1) return;  // one run held it all and wrote the result
+    for (int h = 0; h < s.G; h++) {
+        float m = -INFINITY, l = 0.f, v = 0.f;
+        for (int c = c0; c <= c1; c++) {
+            const size_t e = (size_t)(c * 2 + (c == c0 ? 1 : 0)) * 8 + h;
+            const float mc = a.pml[2 * e], lc = a.pml[2 * e + 1], vc = a.pacc[e * kHeadDim + d];
+            if (mc == -INFINITY) continue;
+            const float mn = fmaxf(m, mc), f = m == -INFINITY ? 0.f : ex2(m - mn), g = ex2(mc - mn);
+            l = l * f + lc * g;
+            v = v * f + vc * g;
+            m = mn;
+        }
+        a.out[(bh0 + h) * kHeadDim + d] = l == 0.f ? 0.f : v / l;
+        if (d == 0) a.lse[bh0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+}
+
+// Runs of the split for sequences up to max_len: two per SM, fewer where the
+// longest possible line has fewer blocks.
+static int num_runs(const PagesShape &s, int max_len)
+{
+    static const int kMaxRuns = 148 * kBlocksPerSm;
+    const long long line = (long long)s.B * s.Hkv * ((max_len + kBlockTok - 1) / kBlockTok);
+    return (int)(line < kMaxRuns ? line : kMaxRuns);
+}
+
+}  // namespace paged
+
+size_t paged_workspace_bytes(const PagesShape &s, int max_len)
+{
+    return (size_t)paged::num_runs(s, max_len) * 2 * 8 * (kHeadDim + 2) * sizeof(float);
+}
+
+cudaError_t launch_paged_attend(const PagesShape &s, const uint16_t *q, const uint16_t *kp, const uint16_t *vp,
+                                const int32_t *table, const int32_t *lens, int max_len, float *out, float *lse,
+                                void *workspace, int32_t *status, cudaStream_t st)
+{
+    paged::Args a;
+    a.s = s;
+    a.q = q;
+    a.kp = kp;
+    a.vp = vp;
+    a.table = table;
+    a.lens = lens;
+    a.max_len = max_len;
+    a.C = paged::num_runs(s, max_len);
+    a.out = out;
+    a.lse = lse;
+    a.pacc = static_cast<float *>(workspace);
+    a.pml = a.pacc + (size_t)a.C * 2 * 8 * kHeadDim;
+    a.status = status;
+    if (a.C > 0) {
+        cudaError_t e = ensure_smem(reinterpret_cast<const void *>(paged::paged_attend_kernel), paged::kRingBytes);
+        if (e != cudaSuccess) return e;
+        e = launch_pdl(paged::paged_attend_kernel, dim3(a.C), dim3(32 * paged::kWarps), paged::kRingBytes, st, a);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(paged::merge_partials_kernel, dim3(s.B * s.Hkv), dim3(kHeadDim), 0, st, a);
+}
+
+}  // namespace mp
