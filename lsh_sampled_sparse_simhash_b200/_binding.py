@@ -160,8 +160,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     import torch
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is None:  # torch.cuda.current_stream() without building its Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def codes_bytes(shape: Shape) -> int:
@@ -292,73 +293,68 @@ class PagesShape:
     max_pages: int
 
     def __post_init__(self):
-        # frozen, so the C struct is made once
-        object.__setattr__(self, "_c", _CPagesShape(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim,
-                                                    self.n_pages, self.page_size, self.max_pages))
+        # frozen, so the C struct and the tensors' shapes are made once
+        def put(name, value):
+            object.__setattr__(self, name, value)
+        put("_c", _CPagesShape(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.n_pages,
+                               self.page_size, self.max_pages))
+        put("_ref", ctypes.byref(self._c))
+        put("_pool", (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim))
+        put("_table", (self.batch, self.max_pages))
+        put("_q", (self.batch, self.n_q_heads, self.head_dim))
 
     def c(self) -> _CPagesShape:
         return self._c
 
 
+def _refuse(t, what: str, dtype, shape, device: int):
+    raise ValueError(f"{what}: expected {tuple(shape)} of {dtype} on cuda:{device} (the current device), got "
+                     f"{tuple(t.shape)}, strides {tuple(t.stride())}, of {t.dtype} on {t.device}")
+
+
 def _arg(t, what: str, dtype, shape, device: int) -> int:
     """Device pointer of a contiguous tensor of this type and shape on the current device."""
-    if not t.is_cuda or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous CUDA tensor {tuple(shape)} of {dtype}, got "
-                         f"{'' if t.is_contiguous() else 'non-contiguous '}{tuple(t.shape)} of {t.dtype} on {t.device}")
-    if t.device.index != device:
-        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{device}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, what, dtype, shape, device)
     return t.data_ptr()
 
 
 def _rows_arg(t, what: str, dtype, shape, device: int):
     """(device pointer, token stride in elements) of [tokens, heads, head_dim] rows whose heads lie side by side."""
-    if not t.is_cuda or t.dtype != dtype or t.shape != shape or \
-            (t.numel() and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != shape[2]))):
-        raise ValueError(f"{what}: expected a CUDA tensor {tuple(shape)} of {dtype} with the heads of a token side by "
-                         f"side, got {tuple(t.shape)}, strides {tuple(t.stride())}, of {t.dtype} on {t.device}")
-    if t.device.index != device:
-        raise ValueError(f"{what}: on {t.device}, but the current device is cuda:{device}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else 0
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, what, dtype, shape, device)
+    rows, heads, d = shape
+    s0, s1, s2 = t.stride()
+    if rows and (s2 != 1 or (heads > 1 and s1 != d)):
+        _refuse(t, what, dtype, shape, device)
+    return t.data_ptr(), s0 if rows > 1 else 0
 
 
-def _status_arg(status, device: int) -> Optional[int]:
-    import torch
-    return None if status is None else _arg(status, "status", torch.int32, status.shape, device)
+def _opt(t, what: str, dtype, shape, device: int) -> Optional[int]:
+    return None if t is None else _arg(t, what, dtype, shape, device)
 
 
 def prompt_attend(shape: PromptShape, q, k, v, cu_lens, out, lse=None, status=None, stream=None):
     """Causal attention over packed prompts: q bf16 [T,Hq,d], k / v bf16 [T,Hkv,d] (token rows may be strided:
     parts of a fused projection), cu_lens int32 [B+1], out bf16 [T,Hq,d], lse fp32 [T,Hq] or None."""
     import torch
-    dev = torch.cuda.current_device()
+    dev, bf16 = torch.cuda.current_device(), torch.bfloat16
     T, Hq, Hkv, d = shape.total, shape.n_q_heads, shape.n_kv_heads, shape.head_dim
-    qp, qs = _rows_arg(q, "q", torch.bfloat16, (T, Hq, d), dev)
-    kp, ks = _rows_arg(k, "k", torch.bfloat16, (T, Hkv, d), dev)
-    vp, vs = _rows_arg(v, "v", torch.bfloat16, (T, Hkv, d), dev)
+    qp, qs = _rows_arg(q, "q", bf16, (T, Hq, d), dev)
+    kp, ks = _rows_arg(k, "k", bf16, (T, Hkv, d), dev)
+    vp, vs = _rows_arg(v, "v", bf16, (T, Hkv, d), dev)
     cs = _CPromptShape(shape.batch, Hq, Hkv, d, T, qs, ks, vs)
     _check(library().mp_prompt_attend(ctypes.byref(cs), qp, kp, vp,
                                       _arg(cu_lens, "cu_lens", torch.int32, (shape.batch + 1,), dev),
-                                      _arg(out, "out", torch.bfloat16, (T, Hq, d), dev),
-                                      None if lse is None else _arg(lse, "lse", torch.float32, (T, Hq), dev),
-                                      _status_arg(status, dev), _stream(stream)), "mp_prompt_attend")
+                                      _arg(out, "out", bf16, (T, Hq, d), dev), _opt(lse, "lse", torch.float32, (T, Hq), dev),
+                                      _opt(status, "status", torch.int32, (1,), dev), _stream(stream)),
+           "mp_prompt_attend")
 
 
 def paged_workspace_bytes(shape: PagesShape, max_len: int) -> int:
     n = ctypes.c_size_t()
-    _check(library().mp_paged_workspace_bytes(ctypes.byref(shape.c()), int(max_len), ctypes.byref(n)),
-           "mp_paged_workspace_bytes")
+    _check(library().mp_paged_workspace_bytes(shape._ref, int(max_len), ctypes.byref(n)), "mp_paged_workspace_bytes")
     return n.value
-
-
-def _pool_args(shape: PagesShape, k_pages, v_pages, dev: int):
-    import torch
-    pool = (shape.n_pages, shape.n_kv_heads, shape.page_size, shape.head_dim)
-    return _arg(k_pages, "k_pages", torch.bfloat16, pool, dev), _arg(v_pages, "v_pages", torch.bfloat16, pool, dev)
-
-
-def _table_arg(shape: PagesShape, page_table, dev: int) -> int:
-    import torch
-    return _arg(page_table, "page_table", torch.int32, (shape.batch, shape.max_pages), dev)
 
 
 def paged_attend(shape: PagesShape, q, k_pages, v_pages, page_table, seq_lens, max_len: int, out, lse, workspace,
@@ -367,17 +363,16 @@ def paged_attend(shape: PagesShape, q, k_pages, v_pages, page_table, seq_lens, m
     seq_lens int32 [B], out fp32 [B,Hq,d], lse fp32 [B,Hq], workspace of paged_workspace_bytes(shape, max_len)
     bytes or more."""
     import torch
-    dev = torch.cuda.current_device()
-    B, Hq, d = shape.batch, shape.n_q_heads, shape.head_dim
-    kp, vp = _pool_args(shape, k_pages, v_pages, dev)
-    _check(library().mp_paged_attend(ctypes.byref(shape.c()), _arg(q, "q", torch.bfloat16, (B, Hq, d), dev), kp, vp,
-                                     _table_arg(shape, page_table, dev),
-                                     _arg(seq_lens, "seq_lens", torch.int32, (B,), dev), int(max_len),
-                                     _arg(out, "out", torch.float32, (B, Hq, d), dev),
-                                     _arg(lse, "lse", torch.float32, (B, Hq), dev),
+    dev, bf16, i32, f32 = torch.cuda.current_device(), torch.bfloat16, torch.int32, torch.float32
+    _check(library().mp_paged_attend(shape._ref, _arg(q, "q", bf16, shape._q, dev),
+                                     _arg(k_pages, "k_pages", bf16, shape._pool, dev),
+                                     _arg(v_pages, "v_pages", bf16, shape._pool, dev),
+                                     _arg(page_table, "page_table", i32, shape._table, dev),
+                                     _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev), int(max_len),
+                                     _arg(out, "out", f32, shape._q, dev), _arg(lse, "lse", f32, shape._q[:2], dev),
                                      _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev),
-                                     workspace.numel() * workspace.element_size(), _status_arg(status, dev),
-                                     _stream(stream)), "mp_paged_attend")
+                                     workspace.numel() * workspace.element_size(),
+                                     _opt(status, "status", i32, (1,), dev), _stream(stream)), "mp_paged_attend")
 
 
 def paged_append(shape: PagesShape, k_new, v_new, page_table, seq_lens, k_pages, v_pages, cu_new=None,
@@ -385,75 +380,73 @@ def paged_append(shape: PagesShape, k_new, v_new, page_table, seq_lens, k_pages,
     """Writes new rows k_new / v_new bf16 [n,Hkv,d] behind the sequences' tokens: one for each sequence (n == B),
     or rows [cu_new[b], cu_new[b+1]) for sequence b (cu_new int32 [B+1]).  advance: seq_lens grow."""
     import torch
-    dev = torch.cuda.current_device()
-    n, Hkv, d = k_new.shape[0], shape.n_kv_heads, shape.head_dim
-    knp, ks = _rows_arg(k_new, "k_new", torch.bfloat16, (n, Hkv, d), dev)
-    vnp, vs = _rows_arg(v_new, "v_new", torch.bfloat16, (n, Hkv, d), dev)
-    kp, vp = _pool_args(shape, k_pages, v_pages, dev)
-    _check(library().mp_paged_append(ctypes.byref(shape.c()), knp, vnp, ks, vs,
-                                     None if cu_new is None else _arg(cu_new, "cu_new", torch.int32, (shape.batch + 1,), dev),
-                                     n, int(bool(advance)), _table_arg(shape, page_table, dev),
-                                     _arg(seq_lens, "seq_lens", torch.int32, (shape.batch,), dev), kp, vp,
-                                     _status_arg(status, dev), _stream(stream)), "mp_paged_append")
-
-
-def _state_args(shape: PagesShape, page_table, seq_lens, refs, dev: int):
-    import torch
-    return (_table_arg(shape, page_table, dev), _arg(seq_lens, "seq_lens", torch.int32, (shape.batch,), dev),
-            _arg(refs, "refs", torch.int32, (shape.n_pages,), dev))
+    dev, bf16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    rows = (k_new.shape[0], shape.n_kv_heads, shape.head_dim)
+    knp, ks = _rows_arg(k_new, "k_new", bf16, rows, dev)
+    vnp, vs = _rows_arg(v_new, "v_new", bf16, rows, dev)
+    _check(library().mp_paged_append(shape._ref, knp, vnp, ks, vs, _opt(cu_new, "cu_new", i32, (shape.batch + 1,), dev),
+                                     rows[0], 1 if advance else 0, _arg(page_table, "page_table", i32, shape._table, dev),
+                                     _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev),
+                                     _arg(k_pages, "k_pages", bf16, shape._pool, dev),
+                                     _arg(v_pages, "v_pages", bf16, shape._pool, dev),
+                                     _opt(status, "status", i32, (1,), dev), _stream(stream)), "mp_paged_append")
 
 
 def pages_reserve(shape: PagesShape, n_new, page_table, seq_lens, refs, status=None, stream=None):
     """Takes the lowest free pages so that sequence b can hold n_new[b] tokens more (n_new int32 [B])."""
     import torch
-    dev = torch.cuda.current_device()
-    _check(library().mp_pages_reserve(ctypes.byref(shape.c()), _arg(n_new, "n_new", torch.int32, (shape.batch,), dev),
-                                      *_state_args(shape, page_table, seq_lens, refs, dev), _status_arg(status, dev),
-                                      _stream(stream)), "mp_pages_reserve")
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    _check(library().mp_pages_reserve(shape._ref, _arg(n_new, "n_new", i32, (shape.batch,), dev),
+                                      _arg(page_table, "page_table", i32, shape._table, dev),
+                                      _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev),
+                                      _arg(refs, "refs", i32, (shape.n_pages,), dev),
+                                      _opt(status, "status", i32, (1,), dev), _stream(stream)), "mp_pages_reserve")
 
 
 def pages_fork(shape: PagesShape, src, dst, page_table, seq_lens, refs, copies, status=None, stream=None):
     """Makes sequence dst[i] a copy of src[i] (int32 [n] both); copies int32 [1+n,4] receives the page copies that
     pages_copy has to make in every layer's pools."""
     import torch
-    dev, n = torch.cuda.current_device(), src.numel()
-    _check(library().mp_pages_fork(ctypes.byref(shape.c()), _arg(src, "src", torch.int32, (n,), dev),
-                                   _arg(dst, "dst", torch.int32, (n,), dev), n,
-                                   *_state_args(shape, page_table, seq_lens, refs, dev),
-                                   _arg(copies, "copies", torch.int32, (1 + n, 4), dev), _status_arg(status, dev),
-                                   _stream(stream)), "mp_pages_fork")
+    dev, i32, n = torch.cuda.current_device(), torch.int32, src.numel()
+    _check(library().mp_pages_fork(shape._ref, _arg(src, "src", i32, (n,), dev), _arg(dst, "dst", i32, (n,), dev), n,
+                                   _arg(page_table, "page_table", i32, shape._table, dev),
+                                   _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev),
+                                   _arg(refs, "refs", i32, (shape.n_pages,), dev),
+                                   _arg(copies, "copies", i32, (1 + n, 4), dev),
+                                   _opt(status, "status", i32, (1,), dev), _stream(stream)), "mp_pages_fork")
 
 
 def pages_free(shape: PagesShape, seqs, page_table, seq_lens, refs, status=None, stream=None):
     """Ends the sequences seqs (int32 [n]): their pages lose a count, their rows become -1, their lengths 0."""
     import torch
-    dev, n = torch.cuda.current_device(), seqs.numel()
-    _check(library().mp_pages_free(ctypes.byref(shape.c()), _arg(seqs, "seqs", torch.int32, (n,), dev), n,
-                                   *_state_args(shape, page_table, seq_lens, refs, dev), _status_arg(status, dev),
-                                   _stream(stream)), "mp_pages_free")
+    dev, i32, n = torch.cuda.current_device(), torch.int32, seqs.numel()
+    _check(library().mp_pages_free(shape._ref, _arg(seqs, "seqs", i32, (n,), dev), n,
+                                   _arg(page_table, "page_table", i32, shape._table, dev),
+                                   _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev),
+                                   _arg(refs, "refs", i32, (shape.n_pages,), dev),
+                                   _opt(status, "status", i32, (1,), dev), _stream(stream)), "mp_pages_free")
 
 
 def pages_compact(shape: PagesShape, page_table, refs, copies, status=None, stream=None):
     """Brings the pages in use to the front of the pools; copies int32 [1+P//2,4] receives the page copies that
     pages_copy has to make in every layer's pools."""
     import torch
-    dev = torch.cuda.current_device()
-    _check(library().mp_pages_compact(ctypes.byref(shape.c()), _table_arg(shape, page_table, dev),
-                                      _arg(refs, "refs", torch.int32, (shape.n_pages,), dev),
-                                      _arg(copies, "copies", torch.int32, (1 + shape.n_pages // 2, 4), dev),
-                                      _status_arg(status, dev), _stream(stream)), "mp_pages_compact")
+    dev, i32 = torch.cuda.current_device(), torch.int32
+    _check(library().mp_pages_compact(shape._ref, _arg(page_table, "page_table", i32, shape._table, dev),
+                                      _arg(refs, "refs", i32, (shape.n_pages,), dev),
+                                      _arg(copies, "copies", i32, (1 + shape.n_pages // 2, 4), dev),
+                                      _opt(status, "status", i32, (1,), dev), _stream(stream)), "mp_pages_compact")
 
 
 def pages_copy(shape: PagesShape, copies, k_pages, v_pages, status=None, stream=None):
     """Copies pages within one layer's pools: copies int32 [1+n,4], entry 0 {count,0,0,0}, then {src, dst, rows, 0}."""
     import torch
-    dev = torch.cuda.current_device()
-    kp, vp = _pool_args(shape, k_pages, v_pages, dev)
-    if copies.dim() != 2 or copies.shape[0] < 1:
-        raise ValueError(f"copies: expected [1 + n, 4], got {tuple(copies.shape)}")
-    _check(library().mp_pages_copy(ctypes.byref(shape.c()), _arg(copies, "copies", torch.int32, (copies.shape[0], 4), dev),
-                                   copies.shape[0] - 1, kp, vp, _status_arg(status, dev), _stream(stream)),
-           "mp_pages_copy")
+    dev, bf16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
+    n = copies.shape[0]
+    _check(library().mp_pages_copy(shape._ref, _arg(copies, "copies", i32, (n, 4), dev), n - 1,
+                                   _arg(k_pages, "k_pages", bf16, shape._pool, dev),
+                                   _arg(v_pages, "v_pages", bf16, shape._pool, dev),
+                                   _opt(status, "status", i32, (1,), dev), _stream(stream)), "mp_pages_copy")
 
 
 def read_status(workspace, stream=None) -> int:

@@ -38,6 +38,7 @@ constexpr int kRowBytes = 256;
 constexpr int kTileBytes = 2 * kTile * kRowBytes;        // K rows, then V rows
 constexpr int kRingBytes = kWarps * kStages * kTileBytes; // 96 KB: two thread blocks per SM
 constexpr int kBlocksPerSm = 2;
+constexpr int kMergeWarps = 4, kMergeBatch = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMargin = 8.f;               // log2 units that a maximum may grow before the sums are rescaled
@@ -112,6 +113,18 @@ __device__ __forceinline__ long long blocks_before(const Args &a, int upto, int 
 // empty).  The run that holds block x is the largest c with c W / C <= x.
 __device__ __forceinline__ int live_runs(long long W, int C) { return (int)min(W, (long long)C); }
 __device__ __forceinline__ int run_of(long long x, long long W, int C) { return (int)(((x + 1) * C - 1) / W); }
+
+// Adds a partial (m, l, v) of weights relative to 2^m2 to another.
+__device__ __forceinline__ void fold(float &m, float &l, float4 &v, float m2, float l2, const float4 &v2)
+{
+    const float mn = fmaxf(m, m2), f = m == -INFINITY ? 0.f : ex2(m - mn), g = ex2(m2 - mn);
+    l = l * f + l2 * g;
+    v.x = v.x * f + v2.x * g;
+    v.y = v.y * f + v2.y * g;
+    v.z = v.z * f + v2.z * g;
+    v.w = v.w * f + v2.w * g;
+    m = mn;
+}
 
 __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel(const Args a)
 {
@@ -275,9 +288,16 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             for (int i = 0; i < 8; i++) {  // 16 dims each
                 uint32_t r0, r1, r2, r3;
                 ldmatrix_x4_trans_s(r0, r1, r2, r3, vt + row_off((lane & 7) + ((lane >> 4) << 3), 2 * i + ((lane >> 3) & 1)));
+                // the tile's own sum, then one rounded add: the tensor core cuts low bits off, not
+                // rounds, and over the thousands of tiles of a long run that adds up (2.5e-5
+                // relative where all tiles went into one accumulator)
+                float d0 = 0.f, d1 = 0.f, d2 = 0.f, d3 = 0.f;
 #pragma unroll
-                for (int j = 2; j >= 0; j--)
-                    mma_bf16_16816(o[i][0], o[i][1], o[i][2], o[i][3], r0, r1, r2, r3, pb[j][0], pb[j][1]);
+                for (int j = 2; j >= 0; j--) mma_bf16_16816(d0, d1, d2, d3, r0, r1, r2, r3, pb[j][0], pb[j][1]);
+                o[i][0] += d0;
+                o[i][1] += d1;
+                o[i][2] += d2;
+                o[i][3] += d3;
             }
             __syncwarp();  // every lane has read the tile before its slot is refilled
             issue(t + kStages - 1);
@@ -342,41 +362,61 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     }
 }
 
-// Joins the partials of the units that several runs share (block = unit,
-// thread = dim), and writes the units without tokens.
-__global__ void __launch_bounds__(kHeadDim) merge_partials_kernel(const Args a)
+// Joins the partials of the units that several runs share, and writes the
+// units without tokens.  A block per (sequence, query head): its warps take
+// the runs in turn (lane = 4 dims), kMergeBatch loads in flight each, then
+// meet in shared memory.
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_partials_kernel(const Args a)
 {
+    __shared__ float red_m[kMergeWarps], red_l[kMergeWarps];
+    __shared__ float4 red_v[kMergeWarps][32];
     const PagesShape &s = a.s;
-    const int unit = blockIdx.x, b = unit / s.Hkv, kvh = unit % s.Hkv, d = threadIdx.x, lane = d & 31;
+    const int bh = blockIdx.x, b = bh / s.Hq, hq = bh % s.Hq, kvh = hq / s.G, h = hq % s.G;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the lengths are older than this kernel's predecessor: read before the wait
     const int nb = blocks_of(clamped_len(a, b));
     const long long before = blocks_before(a, b, lane), W = blocks_before(a, s.B, lane) * s.Hkv;
     const long long x0 = before * s.Hkv + (long long)kvh * nb;
+    int c0 = 0, c1 = 0;
+    if (nb > 0) {
+        const int C = live_runs(W, a.C);
+        c0 = run_of(x0, W, C);
+        c1 = run_of(x0 + nb - 1, W, C);
+    }
     grid_dependency_wait();
-    const size_t bh0 = (size_t)b * s.Hq + (size_t)kvh * s.G;
-    if (nb == 0) {
-        for (int h = 0; h < s.G; h++) {
-            a.out[(bh0 + h) * kHeadDim + d] = 0.f;
-            if (d == 0) a.lse[bh0 + h] = -INFINITY;
+    if (nb > 0 && c0 == c1) return;  // one run held it all and wrote the result
+    float m = -INFINITY, l = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int cb = c0 + warp; nb > 0 && cb <= c1; cb += kMergeWarps * kMergeBatch) {
+        float2 ml[kMergeBatch];
+        float4 acc[kMergeBatch];
+#pragma unroll
+        for (int i = 0; i < kMergeBatch; i++) {
+            const int c = cb + kMergeWarps * i;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (c <= c1) {
+                const size_t e = (size_t)(c * 2 + (c == c0 ? 1 : 0)) * 8 + h;
+                ml[i] = reinterpret_cast<const float2 *>(a.pml)[e];
+                acc[i] = reinterpret_cast<const float4 *>(a.pacc + e * kHeadDim)[lane];
+            }
         }
-        return;
+#pragma unroll
+        for (int i = 0; i < kMergeBatch; i++)
+            if (ml[i].x != -INFINITY) fold(m, l, v, ml[i].x, ml[i].y, acc[i]);
     }
-    const int C = live_runs(W, a.C), c0 = run_of(x0, W, C), c1 = run_of(x0 + nb - 1, W, C);
-    if (c0 == c1) return;  // one run held it all and wrote the result
-    for (int h = 0; h < s.G; h++) {
-        float m = -INFINITY, l = 0.f, v = 0.f;
-        for (int c = c0; c <= c1; c++) {
-            const size_t e = (size_t)(c * 2 + (c == c0 ? 1 : 0)) * 8 + h;
-            const float mc = a.pml[2 * e], lc = a.pml[2 * e + 1], vc = a.pacc[e * kHeadDim + d];
-            if (mc == -INFINITY) continue;
-            const float mn = fmaxf(m, mc), f = m == -INFINITY ? 0.f : ex2(m - mn), g = ex2(mc - mn);
-            l = l * f + lc * g;
-            v = v * f + vc * g;
-            m = mn;
-        }
-        a.out[(bh0 + h) * kHeadDim + d] = l == 0.f ? 0.f : v / l;
-        if (d == 0) a.lse[bh0 + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    red_v[warp][lane] = v;
+    if (lane == 0) {
+        red_m[warp] = m;
+        red_l[warp] = l;
     }
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; w++)
+        if (red_m[w] != -INFINITY) fold(m, l, v, red_m[w], red_l[w], red_v[w][lane]);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    reinterpret_cast<float4 *>(a.out + (size_t)bh * kHeadDim)[lane] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    if (lane == 0) a.lse[bh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 // Runs of the split for sequences up to max_len: two per SM, fewer where the
@@ -419,7 +459,7 @@ cudaError_t launch_paged_attend(const PagesShape &s, const uint16_t *q, const ui
         e = launch_pdl(paged::paged_attend_kernel, dim3(a.C), dim3(32 * paged::kWarps), paged::kRingBytes, st, a);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(paged::merge_partials_kernel, dim3(s.B * s.Hkv), dim3(kHeadDim), 0, st, a);
+    return launch_pdl(paged::merge_partials_kernel, dim3(s.B * s.Hq), dim3(32 * paged::kMergeWarps), 0, st, a);
 }
 
 }  // namespace mp
