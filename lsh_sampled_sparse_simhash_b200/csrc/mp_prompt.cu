@@ -42,6 +42,7 @@ constexpr int kSmemBytes = 1024 + (2 + kSlots) * kTileBytes;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpFix = 10, kWarpTmem = 11;
 constexpr int kThreads = 32 * 12;
 constexpr uint32_t kColS = 0, kColO = 256;    // + 128 t
+constexpr int kPoly = 2;                      // of 8 pairs of weights, those computed by polynomial
 constexpr float kMargin = 8.f;                // log2 units between rescales
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -160,6 +161,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r)
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+// After wait_ld(): the registers of a load may be used from here on (keeps the
+// compiler from moving their use over the wait).
+__device__ __forceinline__ void tie32(uint32_t *r)
+{
+#pragma unroll
+    for (int i = 0; i < 32; i++) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r)
 {
     asm volatile(
@@ -178,11 +194,127 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
+// Two fp32 in a register pair, for the packed add and multiply-add.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// 2^x of a pair on the multiply-add pipe, x <= 126 (below -126: 2^-126).
+// x = n + f with n whole and |f| <= 1/2 (adding and taking away 1.5 2^23
+// rounds to whole numbers), 2^f by a degree-4 polynomial, n added to the
+// exponent.  The coefficients minimise the largest relative error on
+// [-1/2, 1/2] (fitted by Lawson's iteration): 2.7e-6 = 2^-18.5.
+__device__ __forceinline__ void ex2_poly(uint64_t x2, float &y0, float &y1)
+{
+    float x0, x1;
+    unpair(x2, x0, x1);
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x0));  // -126
+    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x1));
+    const uint64_t x = pair(x0, x1);
+    const uint64_t t = add2(x, pair(12582912.f, 12582912.f));
+    const uint64_t f = add2(x, fma2(t, pair(-1.f, -1.f), pair(12582912.f, 12582912.f)));
+    uint64_t p = fma2(f, pair(0.009570102207362652f, 0.009570102207362652f), pair(0.05591785907745361f, 0.05591785907745361f));
+    p = fma2(p, f, pair(0.240247443318367f, 0.240247443318367f));
+    p = fma2(p, f, pair(0.6931217908859253f, 0.6931217908859253f));
+    p = fma2(p, f, pair(0.9999992847442627f, 0.9999992847442627f));
+    float t0, t1, p0, p1;
+    unpair(t, t0, t1);
+    unpair(p, p0, p1);
+    y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+    y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Keys past the row's last visible one (lim: its column within these 32) get
+// a score of -inf.
+__device__ __forceinline__ void hide(uint32_t *u, int lim)
+{
+#pragma unroll
+    for (int c = 0; c < 32; c++)
+        if (c > lim) u[c] = 0xff800000u;
+}
+
+__device__ __forceinline__ void row_max(const uint32_t *u, float *mx)
+{
+#pragma unroll
+    for (int c = 0; c < 32; c += 8)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            mx[i] = max3(mx[i], __uint_as_float(u[c + 2 * i]), __uint_as_float(u[c + 2 * i + 1]));
+}
+
+// The weights of 32 keys of a row, 2^(s scale + ms), as bf16 into 16 columns
+// at p_col, and their sums (of the unrounded values) into l.  NPOLY of every 8
+// pairs go by ex2_poly, the others by the special function unit.
+template <int NPOLY>
+__device__ __forceinline__ void weights(const uint32_t *u, uint64_t scale2, uint64_t ms, uint64_t *l, uint32_t p_col)
+{
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+        const uint64_t x = fma2(pair(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), scale2, ms);
+        float e0, e1;
+        if ((i * NPOLY) % 8 < NPOLY) {
+            ex2_poly(x, e0, e1);
+        } else {
+            unpair(x, e0, e1);
+            e0 = ex2(e0);
+            e1 = ex2(e1);
+        }
+        l[i & 1] = add2(l[i & 1], pair(e0, e1));
+        p[i] = pack_bf16(e0, e1);
+    }
+    tmem_st16(p_col, p);
+}
+
+// All 128 weights of a row: keys 0..63 are in a and b, the others come from
+// TMEM once more (three buffers of 32 scores; all 128 at once spill).
+template <int NPOLY>
+__device__ __forceinline__ void weights_row(uint32_t *a, uint32_t *b, int lim, uint64_t scale2, uint64_t ms, uint64_t *l,
+                                            uint32_t s_col)
+{
+    uint32_t c[32];
+    tmem_ld32(s_col + 64, c);
+    weights<NPOLY>(a, scale2, ms, l, s_col);
+    weights<NPOLY>(b, scale2, ms, l, s_col + 16);
+    wait_ld();
+    tie32(c);
+    if (NPOLY == 0) hide(c, lim - 64);
+    tmem_ld32(s_col + 96, a);
+    weights<NPOLY>(c, scale2, ms, l, s_col + 32);
+    wait_ld();
+    tie32(a);
+    if (NPOLY == 0) hide(a, lim - 96);
+    weights<NPOLY>(a, scale2, ms, l, s_col + 48);
 }
 
 // One item: tokens [m0, m0 + 2 kTok) of the sequence of n tokens whose rows
@@ -385,7 +517,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool stored = r < kTok * G && tok < it.n;
         const int limit = r < kTok * G ? min(tok, it.n - 1) : -1;  // last visible key
         const float scale2 = kLog2e * 0.08838834764831845f;        // log2(e) / sqrt(128)
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY;
+        uint64_t l[2] = {0ull, 0ull};  // four partial sums
         bool ok = true;
         for (int j = 0; j < nt; j++) {
             if (!warp_wait(bar(B_S + t), j & 1, &abort_flag, a.status)) {
@@ -393,27 +526,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             fence_after();
-            uint32_t u[128];
-#pragma unroll
-            for (int c = 0; c < 4; c++) tmem_ld32(s_col + 32 * c, u + 32 * c);
-            wait_ld();
             const int lim = limit - (nt - 1 - j) * kKeys;
-            if (__any_sync(0xffffffffu, lim < kKeys - 1)) {
+            const bool masked = __any_sync(0xffffffffu, lim < kKeys - 1);
+            uint32_t ua[32], ub[32];
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 128; c++)
-                    if (c > lim) u[c] = 0xff800000u;  // -inf
+            for (int c = 2; c >= 0; c -= 2) {
+                tmem_ld32(s_col + 32 * c, ua);
+                tmem_ld32(s_col + 32 * c + 32, ub);
+                wait_ld();
+                tie32(ua);
+                tie32(ub);
+                if (masked) {
+                    hide(ua, lim - 32 * c);
+                    hide(ub, lim - 32 * c - 32);
+                }
+                row_max(ua, mx);
+                row_max(ub, mx);
             }
-            float mx = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 128; c++) mx = fmaxf(mx, __uint_as_float(u[c]));
-            mx *= scale2;
-            const bool grow = mx > m + kMargin;
+            const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale2;
+            const bool grow = top > m + kMargin;
             if (__any_sync(0xffffffffu, grow)) {
-                const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - mx)) : 1.f;
-                if (grow) m = mx;
-                l *= f;
+                const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
+                if (grow) m = top;
+                l[0] = fma2(l[0], pair(f, f), 0ull);
+                l[1] = fma2(l[1], pair(f, f), 0ull);
                 if (j > 0) {  // every product into O so far is complete (it was issued before this S)
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; c++) {
                         uint32_t o[32];
                         tmem_ld32(o_col + 32 * c, o);
@@ -424,18 +563,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            const float ms = m == -INFINITY ? 0.f : m;
-#pragma unroll
-            for (int c = 0; c < 128; c += 64) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; i++) {
-                    const float e0 = ex2(fmaf(__uint_as_float(u[c + 2 * i]), scale2, -ms));
-                    const float e1 = ex2(fmaf(__uint_as_float(u[c + 2 * i + 1]), scale2, -ms));
-                    l += e0 + e1;
-                    p[i] = pack_bf16(e0, e1);
-                }
-                tmem_st32(s_col + c / 2, p);
+            const float ms = m == -INFINITY ? 0.f : -m;
+            const uint64_t scale_2 = pair(scale2, scale2), ms_2 = pair(ms, ms);
+            // hidden keys have to come out as 0 and not as 2^-126: a masked tile takes the exact path
+            if (masked) {
+                weights_row<0>(ua, ub, lim, scale_2, ms_2, l, s_col);
+            } else {
+                weights_row<kPoly>(ua, ub, lim, scale_2, ms_2, l, s_col);
             }
             wait_st();
             fence_before();
@@ -445,7 +579,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && warp_wait(bar(B_O + t), 0, &abort_flag, a.status)) {
             fence_after();
             const size_t row = (size_t)(it.row0 + tok) * a.s.Hq + (size_t)it.kvh * G + head;
-            const float inv = 1.f / l;
+            float l0, l1;
+            unpair(add2(l[0], l[1]), l0, l1);
+            const float sum = l0 + l1, inv = 1.f / sum;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * kHeadDim);
             uint32_t o[128];
 #pragma unroll
@@ -461,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
                 }
             }
-            if (stored && a.lse) a.lse[row] = (m + log2f(l)) * kLn2;
+            if (stored && a.lse) a.lse[row] = (m + log2f(sum)) * kLn2;
         }
     }
     fence_before();
