@@ -10,17 +10,19 @@
 // An item is 2 kTok tokens of one sequence and one kv head: two 128-row query
 // tiles whose rows are (token, head of the group), so the G heads share every
 // K and V tile (kTok = 128 / G tokens a tile).  Key tiles are 128 tokens,
-// walked from the last visible one down to the first.
+// walked from the last visible one down to the first; a query tile joins at
+// its own last one.  One block per SM takes items in turn, longest first,
+// every second round in reverse (so the blocks' sums of work come out alike):
 //   warps 0-3, 4-7  softmax of query tile 0, 1: thread = row.  S from TMEM,
-//                   maximum, P = 2^(s - m) in bf16 back into the columns of S,
-//                   sum; rescaling of O (TMEM) only when the maximum grows by
-//                   more than 2^8; at the end O / sum to memory.
-//   warp 8          MMA issuer (one thread): S = Q K^T, O += P V with P as the
-//                   A operand in TMEM; the two tiles alternate, so one tile's
-//                   products run under the other's softmax.
-//   warp 9          TMA producer: Q (both tiles), then the ring of K and V tiles.
+//                   P = 2^(s - m) in bf16 back into the columns of S, sum; at
+//                   the end of an item O / sum to memory.
+//   warp 8          MMA issuer: S = Q K^T, O += P V with P as the A operand in
+//                   TMEM; the two tiles alternate, so one tile's products run
+//                   under the other's softmax, and the first S of the next
+//                   item under the last softmax of this one.
+//   warp 9          TMA producer: Q (both tiles), the ring of K and V tiles.
 //   warp 10         zeroes the rows of the last V tile behind the sequence's end.
-//   warp 11         holds the TMEM allocation.
+//   warp 11         finds the next items; holds the TMEM allocation.
 // TMEM: S0, S1, O0, O1, 128 columns each.
 //
 // Every wait is bounded (1 s); on expiry MP_ERR_CUDA is recorded and the block
@@ -38,12 +40,21 @@ constexpr int kKeys = 128;                    // keys of a tile
 constexpr int kHalfBytes = 128 * 128;         // 128 rows x 64 elements
 constexpr int kTileBytes = 2 * kHalfBytes;    // 32 KB
 constexpr int kSlots = 5;                     // ring of K and V tiles
+constexpr int kItems = 4;                     // items known ahead
+constexpr int kFixes = 4;                     // more than the V tiles that the ring can hold
 constexpr int kSmemBytes = 1024 + (2 + kSlots) * kTileBytes;
-constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpFix = 10, kWarpTmem = 11;
+constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpFix = 10, kWarpItems = 11;
 constexpr int kThreads = 32 * 12;
 constexpr uint32_t kColS = 0, kColO = 256;    // + 128 t
-constexpr int kPoly = 2;                      // of 8 pairs of weights, those computed by polynomial
-constexpr float kMargin = 8.f;                // log2 units between rescales
+#ifndef KPOLY
+#define KPOLY 2
+#endif
+constexpr int kPoly = KPOLY;                      // of 8 pairs of weights, those computed by polynomial
+#ifndef HALVES
+#define HALVES 1
+#endif
+constexpr bool kHalves = HALVES;
+constexpr float kMargin = 24.f;               // log2 units that a score may exceed its row's reference by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -53,20 +64,23 @@ struct Args {
     uint16_t *out;
     float *lse;
     int32_t *status;
-    int n_items;  // upper bound
 };
 
 enum {
-    B_Q = 0,                 // [2] query tile landed
-    B_KV = B_Q + 2,          // [kSlots] K or V tile landed
-    B_FREE = B_KV + kSlots,  // [kSlots] products on the slot complete
-    B_S = B_FREE + kSlots,   // [2] S in TMEM (and all products before it complete)
-    B_P = B_S + 2,           // [2] P in TMEM, O rescaled (4 warps)
-    B_O = B_P + 2,           // [2] the item's last product into O complete
-    B_FIX = B_O + 2,         // last V tile's rows behind the sequence's end zeroed
-    B_END = B_FIX + 1,       // teardown
+    B_Q = 0,                   // [2] query tile landed
+    B_QFREE = B_Q + 2,         // [2] the item's last product on it complete
+    B_KV = B_QFREE + 2,        // [kSlots] K or V tile landed (and its rows behind the sequence's end zeroed)
+    B_FREE = B_KV + kSlots,    // [kSlots] products on the slot complete
+    B_S = B_FREE + kSlots,     // [2] S in TMEM (and all products before it complete)
+    B_P = B_S + 2,             // [2][2] P of keys 0-63, 64-127 in TMEM, O rescaled (4 warps each)
+    B_O = B_P + 4,           // [2] the item's last product into O complete
+    B_FIX = B_O + 2,           // [kFixes] V tile landed that has rows behind the sequence's end, in turn
+    B_ITEM = B_FIX + kFixes,   // [kItems] item known
+    B_TAKEN = B_ITEM + kItems, // [kItems] item done with by all roles
+    B_END = B_TAKEN + kItems,  // teardown
     kBars = B_END + 1
 };
+constexpr int kRoles = 8 + 3;  // warps that read an item
 
 __device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, volatile int *abort_flag, int32_t *status)
 {
@@ -96,6 +110,14 @@ __device__ __noinline__ void wait_teardown(uint32_t a, uint32_t parity)
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(a, parity))
         if (globaltimer() - t0 > kWaitLimitNs) return;
+}
+
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int x, int y, int z)
@@ -223,30 +245,44 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// 2^x of a pair on the multiply-add pipe, x <= 126 (below -126: 2^-126).
-// x = n + f with n whole and |f| <= 1/2 (adding and taking away 1.5 2^23
-// rounds to whole numbers), 2^f by a degree-4 polynomial, n added to the
-// exponent.  The coefficients minimise the largest relative error on
-// [-1/2, 1/2] (fitted by Lawson's iteration): 2.7e-6 = 2^-18.5.
-__device__ __forceinline__ void ex2_poly(uint64_t x2, float &y0, float &y1)
-{
-    float x0, x1;
-    unpair(x2, x0, x1);
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x0));  // -126
-    asm("max.NaN.f32 %0, %0, 0fC2FC0000;" : "+f"(x1));
-    const uint64_t x = pair(x0, x1);
-    const uint64_t t = add2(x, pair(12582912.f, 12582912.f));
-    const uint64_t f = add2(x, fma2(t, pair(-1.f, -1.f), pair(12582912.f, 12582912.f)));
-    uint64_t p = fma2(f, pair(0.009570102207362652f, 0.009570102207362652f), pair(0.05591785907745361f, 0.05591785907745361f));
-    p = fma2(p, f, pair(0.240247443318367f, 0.240247443318367f));
-    p = fma2(p, f, pair(0.6931217908859253f, 0.6931217908859253f));
-    p = fma2(p, f, pair(0.9999992847442627f, 0.9999992847442627f));
-    float t0, t1, p0, p1;
-    unpair(t, t0, t1);
-    unpair(p, p0, p1);
-    y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-    y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-}
+// 2^x of a pair on the multiply-add pipe, x <= 126.  x = n + f with n whole
+// and |f| <= 1/2 (adding and taking away 1.5 2^23 rounds to whole numbers),
+// 2^f by a polynomial, n added to the exponent.  The coefficients minimise the
+// largest relative error on [-1/2, 1/2] among those with value 1 at 0 (fitted
+// by Lawson's iteration): 2.9e-6 = 2^-18.4.  Below -126 the result is between
+// 0 and 2^-126, from -127 on exactly 0 (the 1 at 0 loses its whole exponent).
+// In three parts, so that they can be spread between other instructions.
+struct Ex2Poly {
+    uint64_t t, f, p;
+    __device__ __forceinline__ void split(uint64_t x2)
+    {
+        float x0, x1;
+        unpair(x2, x0, x1);
+        asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127
+        asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
+        const uint64_t x = pair(x0, x1);
+        t = add2(x, pair(12582912.f, 12582912.f));
+        f = add2(x, fma2(t, pair(-1.f, -1.f), pair(12582912.f, 12582912.f)));
+    }
+    __device__ __forceinline__ void first()
+    {
+        p = fma2(f, pair(0.009582852944731712f, 0.009582852944731712f), pair(0.055906426161527634f, 0.055906426161527634f));
+        p = fma2(p, f, pair(0.24024099111557007f, 0.24024099111557007f));
+    }
+    __device__ __forceinline__ void second()
+    {
+        p = fma2(p, f, pair(0.6931241750717163f, 0.6931241750717163f));
+        p = fma2(p, f, pair(1.f, 1.f));
+    }
+    __device__ __forceinline__ void join(float &y0, float &y1) const
+    {
+        float t0, t1, p0, p1;
+        unpair(t, t0, t1);
+        unpair(p, p0, p1);
+        y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+        y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
+    }
+};
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
@@ -273,8 +309,8 @@ __device__ __forceinline__ void row_max(const uint32_t *u, float *mx)
 }
 
 // The weights of 32 keys of a row, 2^(s scale + ms), as bf16 into 16 columns
-// at p_col, and their sums (of the unrounded values) into l.  NPOLY of every 8
-// pairs go by ex2_poly, the others by the special function unit.
+// at p_col, their sums (of the unrounded values) into l.  NPOLY of every 8
+// pairs go by Ex2Poly, the others by the special function unit.
 template <int NPOLY>
 __device__ __forceinline__ void weights(const uint32_t *u, uint64_t scale2, uint64_t ms, uint64_t *l, uint32_t p_col)
 {
@@ -284,7 +320,11 @@ __device__ __forceinline__ void weights(const uint32_t *u, uint64_t scale2, uint
         const uint64_t x = fma2(pair(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), scale2, ms);
         float e0, e1;
         if ((i * NPOLY) % 8 < NPOLY) {
-            ex2_poly(x, e0, e1);
+            Ex2Poly poly;
+            poly.split(x);
+            poly.first();
+            poly.second();
+            poly.join(e0, e1);
         } else {
             unpair(x, e0, e1);
             e0 = ex2(e0);
@@ -296,32 +336,94 @@ __device__ __forceinline__ void weights(const uint32_t *u, uint64_t scale2, uint
     tmem_st16(p_col, p);
 }
 
-// All 128 weights of a row: keys 0..63 are in a and b, the others come from
-// TMEM once more (three buffers of 32 scores; all 128 at once spill).
-template <int NPOLY>
-__device__ __forceinline__ void weights_row(uint32_t *a, uint32_t *b, int lim, uint64_t scale2, uint64_t ms, uint64_t *l,
-                                            uint32_t s_col)
+// The warp's writes to TMEM so far are complete: tells the MMA issuer.
+__device__ __forceinline__ void publish(uint32_t bar, int lane)
 {
-    uint32_t c[32];
+    wait_st();
+    fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// A key tile of every row of a warp: P into the columns of S, 64 keys at a
+// time, each half published on its own barrier, the sums into l.  lim: the
+// row's last visible key (masked: some row of the warp does not see all).
+// m: the reference (log2 units) of the row's sums, kept while no score passes
+// it by kMargin (bf16 and fp32 hold their relative precision there, and no sum
+// comes near fp32's range); past that, or with no reference yet, the tile's
+// maximum takes its place and l and O are rescaled (`o_used`: O holds
+// something; all products into it are complete, as they were issued before
+// this S).  Scores are read twice from TMEM, through three buffers of 32: all
+// 128 at once spill.
+__device__ __forceinline__ void row_tile(float &m, uint64_t *l, int lim, bool masked, bool o_used, uint32_t s_col,
+                                         uint32_t o_col, uint32_t p_bar, int lane)
+{
+    const float scale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
+    uint32_t a[32], b[32], c[32];
+    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int k = 2; k >= 0; k -= 2) {
+        tmem_ld32(s_col + 32 * k, a);
+        tmem_ld32(s_col + 32 * k + 32, b);
+        wait_ld();
+        tie32(a);
+        tie32(b);
+        if (masked) {
+            hide(a, lim - 32 * k);
+            hide(b, lim - 32 * k - 32);
+        }
+        row_max(a, mx);
+        row_max(b, mx);
+    }
+    const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale;
+    const bool grow = top > m + kMargin;
+    if (__any_sync(0xffffffffu, grow)) {
+        const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
+        if (grow) m = top;
+        l[0] = fma2(l[0], pair(f, f), 0ull);
+        l[1] = fma2(l[1], pair(f, f), 0ull);
+        if (o_used) {
+#pragma unroll 1
+            for (int k = 0; k < 4; k++) {
+                tmem_ld32(o_col + 32 * k, c);
+                wait_ld();
+                tie32(c);
+#pragma unroll
+                for (int i = 0; i < 32; i++) c[i] = __float_as_uint(__uint_as_float(c[i]) * f);
+                tmem_st32(o_col + 32 * k, c);
+            }
+        }
+    }
+    const float neg = m == -INFINITY ? 0.f : -m;
+    const uint64_t scale2 = pair(scale, scale), ms = pair(neg, neg);
     tmem_ld32(s_col + 64, c);
-    weights<NPOLY>(a, scale2, ms, l, s_col);
-    weights<NPOLY>(b, scale2, ms, l, s_col + 16);
+    weights<kPoly>(a, scale2, ms, l, s_col);
+    weights<kPoly>(b, scale2, ms, l, s_col + 16);
+    if (kHalves) publish(p_bar, lane);
     wait_ld();
     tie32(c);
-    if (NPOLY == 0) hide(c, lim - 64);
+    if (masked) hide(c, lim - 64);
     tmem_ld32(s_col + 96, a);
-    weights<NPOLY>(c, scale2, ms, l, s_col + 32);
+    weights<kPoly>(c, scale2, ms, l, s_col + 32);
     wait_ld();
     tie32(a);
-    if (NPOLY == 0) hide(a, lim - 96);
-    weights<NPOLY>(a, scale2, ms, l, s_col + 48);
+    if (masked) hide(a, lim - 96);
+    weights<kPoly>(a, scale2, ms, l, s_col + 48);
+    publish(p_bar + 8, lane);
 }
 
 // One item: tokens [m0, m0 + 2 kTok) of the sequence of n tokens whose rows
-// start at row0.
+// start at row0 (n = 0: no more items).
 struct Item {
     int kvh, row0, n, m0;
 };
+
+// Key tiles that query tile t (kTok tokens) sees; 0: it has no token.
+__device__ __forceinline__ int key_tiles(const Item &it, int t, int kTok)
+{
+    const int first = it.m0 + t * kTok;
+    return first < it.n ? (min(first + kTok, it.n) - 1) / kKeys + 1 : 0;
+}
 
 // Rows of sequence b; a pair of entries that breaks the rules holds none.
 __device__ __forceinline__ int seq_rows(const Args &a, int b, int &row0)
@@ -331,44 +433,93 @@ __device__ __forceinline__ int seq_rows(const Args &a, int b, int &row0)
     return lo < 0 || hi < lo || hi > a.s.T ? 0 : hi - lo;
 }
 
-// The item of rank r, longest rows first.  With c_b = ceil(n_b / M) items in
+// Items by rank, longest rows first.  With c_b = ceil(n_b / M) items in
 // sequence b (M tokens each), F(x) = sum_b max(0, c_b - x) items have index >=
 // x in their sequence; rank r has the largest index x with F(x) > r, in the
-// (r - F(x + 1))-th sequence that has one.  Run by one warp; false: no such item.
-__device__ __forceinline__ bool item_of(const Args &a, int r, int M, int lane, Item &it)
-{
-    const int Hkv = a.s.Hkv, B = a.s.B;
-    it.kvh = r % Hkv;
-    r /= Hkv;
-    auto F = [&](int x) {
+// (r - F(x + 1))-th sequence that has one.  Ranks are asked for in rising
+// order, so x only falls.  Run by one warp.
+template <int M>
+struct ItemList {
+    const Args &a;
+    int lane, x, fx;  // F(x) = fx, and F(x + 1) = above
+    int above;
+    __device__ __forceinline__ int F(int y) const
+    {
         int f = 0, row0;
-        for (int b = lane; b < B; b += 32) f += max((seq_rows(a, b, row0) + M - 1) / M - x, 0);
+        for (int b = lane; b < a.s.B; b += 32) f += max((seq_rows(a, b, row0) + M - 1) / M - y, 0);
         return __reduce_add_sync(0xffffffffu, f);
-    };
-    if (F(0) <= r) return false;
-    int lo = 0, hi = (a.s.T + M - 1) / M;  // F(lo) > r >= F(hi)
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (F(mid) > r) lo = mid;
-        else hi = mid;
     }
-    int k = r - F(lo + 1);
-    for (int b0 = 0; b0 < B; b0 += 32) {
-        int row0 = 0, n = 0;
-        if (b0 + lane < B) n = seq_rows(a, b0 + lane, row0);
-        const unsigned has = __ballot_sync(0xffffffffu, (n + M - 1) / M > lo);
-        const int here = __popc(has);
-        if (k < here) {
-            const int l = (int)__fns(has, 0, k + 1);
-            it.n = __shfl_sync(0xffffffffu, n, l);
-            it.row0 = __shfl_sync(0xffffffffu, row0, l);
-            it.m0 = lo * M;
-            return true;
+    __device__ __forceinline__ ItemList(const Args &args, int ln) : a(args), lane(ln)
+    {
+        int most = 0, row0;
+        for (int b = lane; b < a.s.B; b += 32) most = max(most, (seq_rows(a, b, row0) + M - 1) / M);
+        x = __reduce_max_sync(0xffffffffu, most);
+        fx = above = 0;
+    }
+    __device__ __forceinline__ bool get(int r, Item &it)
+    {
+        it.kvh = r % a.s.Hkv;
+        r /= a.s.Hkv;
+        while (fx <= r) {
+            if (x == 0) return false;
+            x--;
+            above = fx;
+            fx = F(x);
         }
-        k -= here;
+        int k = r - above;
+        for (int b0 = 0; b0 < a.s.B; b0 += 32) {
+            int row0 = 0, n = 0;
+            if (b0 + lane < a.s.B) n = seq_rows(a, b0 + lane, row0);
+            const unsigned has = __ballot_sync(0xffffffffu, (n + M - 1) / M > x);
+            const int here = __popc(has);
+            if (k < here) {
+                const int l = (int)__fns(has, 0, k + 1);
+                it.n = __shfl_sync(0xffffffffu, n, l);
+                it.row0 = __shfl_sync(0xffffffffu, row0, l);
+                it.m0 = x * M;
+                return true;
+            }
+            k -= here;
+        }
+        return false;
     }
-    return false;
-}
+};
+
+// A role's walk over the block's items.
+struct ItemWalk {
+    Item *items;
+    uint32_t bar0;
+    int k;
+    volatile int *abort_flag;
+    int32_t *status;
+    // Waits for the next item; false at the end.
+    __device__ __forceinline__ bool next(Item &it)
+    {
+        if (!warp_wait(bar0 + 8u * (B_ITEM + k % kItems), (k / kItems) & 1, abort_flag, status)) return false;
+        it = items[k % kItems];
+        return it.n > 0;
+    }
+    // The warp has read all that it needs of the item.
+    __device__ __forceinline__ void done(int lane)
+    {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar0 + 8u * (B_TAKEN + k % kItems));
+        k++;
+    }
+};
+
+// A running tile number of the ring: slot and parity.
+struct Slot {
+    int slot = 0;
+    uint32_t par = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == kSlots) {
+            slot = 0;
+            par ^= 1u;
+        }
+    }
+};
 
 template <int G>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -379,223 +530,292 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ uint32_t tmem_sh;
-    __shared__ Item item_sh;
-    __shared__ int live_sh;
+    __shared__ Item items[kItems];
     __shared__ volatile int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t q_smem = smem, ring = smem + 2 * kTileBytes;
     const uint32_t bar0 = smem_u32(&bars[0]);
     auto bar = [&](int i) { return bar0 + 8u * (uint32_t)i; };
-    grid_dependency_wait();
+    auto wwait = [&](int i, uint32_t parity) { return warp_wait(bar(i), parity, &abort_flag, a.status); };
 
-    if (blockIdx.x == 0)
-        for (int b = tid; b < a.s.B; b += kThreads) {
-            const int lo = a.cu[b], hi = a.cu[b + 1];
-            if (lo < 0 || hi < lo || hi > a.s.T) set_status(a.status, MP_ERR_CAPACITY);
-        }
-    if (warp == 0) {
-        Item it;
-        const bool live = item_of(a, blockIdx.x, 2 * kTok, lane, it);
-        if (lane == 0) {
-            live_sh = live;
-            item_sh = it;
-            abort_flag = 0;
-            for (int i = 0; i < kBars; i++) mbar_init(bar(i), i == B_P || i == B_P + 1 ? 4 : 1);
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        }
+    if (tid == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < kBars; i++)
+            mbar_init(bar(i), i >= B_P && i < B_P + 4 ? 4 : i >= B_TAKEN && i < B_TAKEN + kItems ? kRoles : 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __syncthreads();
-    if (!live_sh) return;
-    if (warp == kWarpTmem) {
+    // rows of a query tile that no (token, head) fills: the copies never write them
+    if (kTok * G < kRows && warp < 8) {
+        for (int i = tid; i < 2 * 2 * (kRows - kTok * G) * 8; i += 256) {
+            const int piece = i & 7, h = (i >> 3) & 3, r = kTok * G + (i >> 5);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(q_smem + (uint32_t)(h * kHalfBytes + r * 128 + piece * 16)),
+                         "r"(0)
+                         : "memory");
+        }
+        fence_proxy_async_smem();
+    }
+    grid_dependency_wait();
+    if (warp == kWarpItems) {  // after the wait: a kernel before this one may hold TMEM until it ends
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&tmem_sh)), "r"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = tmem_sh;
-    const Item it = item_sh;
-    const int last_tok = min(it.m0 + 2 * kTok, it.n) - 1;  // the item's last token
-    const int nt = last_tok / kKeys + 1;                   // key tiles, walked from nt - 1 to 0
-    const bool fix = nt * kKeys > it.n;                    // the first of them has rows behind the sequence's end
+    constexpr uint32_t tmem = 0;  // the base of an allocation of all columns
+    ItemWalk walk{items, bar0, 0, &abort_flag, a.status};
+    Item it;
 
-    if (warp == kWarpLoad && lane == 0) {
-        // ------------------------------------------------------- producer ----
-        for (int t = 0; t < 2; t++) {
-            mbar_expect_tx(bar(B_Q + t), 2 * kTok * G * 128);
-            for (int h = 0; h < 2; h++)
-                tma_3d(q_smem + t * kTileBytes + h * kHalfBytes, &mq, bar(B_Q + t), 64 * h, it.kvh * G,
-                       it.row0 + it.m0 + t * kTok);
-            if (t == 0) {  // the first K tile before the second query tile
-                mbar_expect_tx(bar(B_KV), kTileBytes);
-                for (int h = 0; h < 2; h++)
-                    tma_3d(ring + h * kHalfBytes, &mk, bar(B_KV), 64 * h, it.kvh, it.row0 + (nt - 1) * kKeys);
+    if (warp == kWarpItems) {
+        // ----------------------------------------------------------- items ----
+        if (blockIdx.x == 0)
+            for (int b = lane; b < a.s.B; b += 32) {
+                const int lo = a.cu[b], hi = a.cu[b + 1];
+                if (lo < 0 || hi < lo || hi > a.s.T) set_status(a.status, MP_ERR_CAPACITY);
             }
+        ItemList<2 * kTok> list(a, lane);
+        const int C = gridDim.x, c = blockIdx.x;
+        for (int k = 0;; k++) {
+            const bool live = list.get(k * C + ((k & 1) ? C - 1 - c : c), it);
+            if (k >= kItems && !wwait(B_TAKEN + k % kItems, (k / kItems - 1) & 1)) break;
+            if (!live) it.n = 0;
+            if (lane == 0) {
+                items[k % kItems] = it;
+                mbar_arrive(bar(B_ITEM + k % kItems));
+            }
+            if (!live) break;
         }
-        int last = 0;
-        for (int i = 1; i < 2 * nt; i++) {  // tile i: K (even) or V (odd) of key tile nt - 1 - i / 2
-            const int slot = i % kSlots;
-            if (i >= kSlots && !wait(bar(B_FREE + slot), (i / kSlots - 1) & 1, &abort_flag, a.status)) break;
-            mbar_expect_tx(bar(B_KV + slot), kTileBytes);
-            for (int h = 0; h < 2; h++)
-                tma_3d(ring + slot * kTileBytes + h * kHalfBytes, (i & 1) ? &mv : &mk, bar(B_KV + slot), 64 * h, it.kvh,
-                       it.row0 + (nt - 1 - i / 2) * kKeys);
-            last = i;
+    } else if (warp == kWarpLoad) {
+        // -------------------------------------------------------- producer ----
+        Slot sl;
+        int used = 0;             // tiles issued so far (kSlots and more: wait for the slot)
+        int nq[2] = {0, 0};       // items that query tile t took part in
+        int n_fix = 0;            // V tiles handed to the warp that zeroes
+        bool ok = true;
+        auto load_kv = [&](const CUtensorMap *m, int kt, bool fix) {
+            const uint32_t landed = bar(fix ? B_FIX + n_fix % kFixes : B_KV + sl.slot);
+            n_fix += fix;
+            if (used >= kSlots && !wwait(B_FREE + sl.slot, sl.par ^ 1u)) return false;
+            if (elect_one()) {
+                mbar_expect_tx(landed, kTileBytes);
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    tma_3d(ring + sl.slot * kTileBytes + h * kHalfBytes, m, landed, 64 * h, it.kvh, it.row0 + kt * kKeys);
+            }
+            __syncwarp();
+            sl.next();
+            used = min(used + 1, kSlots);
+            return true;
+        };
+        while (ok && walk.next(it)) {
+            const int nt = max(key_tiles(it, 0, kTok), key_tiles(it, 1, kTok));
+            const int first = key_tiles(it, 0, kTok) == nt ? 0 : 1;  // the query tile that needs the first K tile
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int t = i ^ first;
+                if (ok && key_tiles(it, t, kTok) > 0) {
+                    ok = nq[t] == 0 || wwait(B_QFREE + t, (nq[t] - 1) & 1);
+                    if (ok && elect_one()) {
+                        mbar_expect_tx(bar(B_Q + t), 2 * kTok * G * 128);
+                        for (int h = 0; h < 2; h++)
+                            tma_3d(q_smem + t * kTileBytes + h * kHalfBytes, &mq, bar(B_Q + t), 64 * h, it.kvh * G,
+                                   it.row0 + it.m0 + t * kTok);
+                    }
+                    __syncwarp();
+                    if (ok) nq[t]++;
+                }
+                if (i == 0) ok = ok && load_kv(&mk, nt - 1, false);
+            }
+            for (int kt = nt - 1; kt >= 0 && ok; kt--)
+                ok = load_kv(&mv, kt, (kt + 1) * kKeys > it.n) && (kt == 0 || load_kv(&mk, kt - 1, false));
+            walk.done(lane);
         }
         // own copies land before the block leaves
-        wait_teardown(bar(B_Q), 0);
-        wait_teardown(bar(B_Q + 1), 0);
-        for (int i = max(0, last - kSlots + 1); i <= last; i++) wait_teardown(bar(B_KV + i % kSlots), (i / kSlots) & 1);
-    } else if (warp == kWarpMma && lane == 0) {
-        // ------------------------------------------------------------ MMA ----
+        for (int t = 0; t < 2; t++)
+            if (nq[t] > 0) wait_teardown(bar(B_Q + t), (nq[t] - 1) & 1);
+        if (n_fix > 0) wait_teardown(bar(B_FIX + (n_fix - 1) % kFixes), ((n_fix - 1) / kFixes) & 1);
+        for (int i = 0; i < used; i++) {  // the last `used` tiles, from the latest back
+            sl.slot = sl.slot == 0 ? kSlots - 1 : sl.slot - 1;
+            if (sl.slot == kSlots - 1) sl.par ^= 1u;
+            wait_teardown(bar(B_KV + sl.slot), sl.par);
+        }
+    } else if (warp == kWarpMma) {
+        // ------------------------------------------------------------- MMA ----
+        // The whole warp walks the loop and one elected lane issues, so that
+        // descriptors and addresses stay in uniform registers (a lone lane's
+        // have to be moved there before every product: 90 cycles a product
+        // against the 64 that it takes).
+        const uint64_t q_desc = desc_kmajor(q_smem), k_desc = desc_kmajor(ring), v_desc = desc_mnmajor(ring);
         auto qk = [&](int t, int slot) {
+            const uint64_t qd = q_desc + (uint64_t)(t * (kTileBytes >> 4));
+            const uint64_t kd = k_desc + (uint64_t)(slot * (kTileBytes >> 4));
 #pragma unroll
             for (int ks = 0; ks < 8; ks++) {
-                const uint32_t off = (uint32_t)((ks >> 2) * kHalfBytes + (ks & 3) * 32);
-                mma_ss(tmem + kColS + 128 * t, desc_kmajor(q_smem + t * kTileBytes + off),
-                       desc_kmajor(ring + slot * kTileBytes + off), idesc(false), ks > 0);
+                const uint64_t off = (uint64_t)(((ks >> 2) * kHalfBytes + (ks & 3) * 32) >> 4);
+                mma_ss(tmem + kColS + 128 * t, qd + off, kd + off, idesc(false), ks > 0);
             }
         };
-        auto pv = [&](int t, int slot, bool accum) {
+        auto pv = [&](int t, int slot, int half, bool accum) {
+            const uint64_t vd = v_desc + (uint64_t)(slot * (kTileBytes >> 4));
 #pragma unroll
-            for (int ks = 0; ks < 8; ks++)
-                mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * ks,
-                       desc_mnmajor(ring + slot * kTileBytes + ks * 2048), idesc(true), accum || ks > 0);
+            for (int ks = 4 * half; ks < 4 * half + 4; ks++)
+                mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * ks, vd + (uint64_t)(ks * (2048 >> 4)),
+                       idesc(true), accum || ks > 0);
         };
-        auto arrived = [&](int i) { return wait(bar(B_KV + i % kSlots), (i / kSlots) & 1, &abort_flag, a.status); };
-        bool ok = true;
-        for (int t = 0; t < 2 && ok; t++) {
-            ok = wait(bar(B_Q + t), 0, &abort_flag, a.status) && arrived(0);
-            if (!ok) break;
-            fence_after();
-            qk(t, 0);
-            commit(bar(B_S + t));
+        const bool leader = elect_one();
+        // A wait that only the tensor pipe's pace should hold up: no vote over
+        // the warp; after an abort every wait returns at once and the walk over
+        // the items ends.
+        auto lwait = [&](int i, uint32_t parity) {
+            if (!mbar_try_wait(bar(i), parity)) wait_slow(bar(i), parity, &abort_flag, a.status);
+        };
+        // A step is one key tile of one item.  Each round does the P V products
+        // of a step and the Q K^T products of the one after it (of the next
+        // item at an item's end), query tile by query tile.
+        Slot vsl, ksl;  // V tile of the step, K tile of the next; K and V tiles alternate in the ring
+        uint32_t q_par[2] = {0, 0}, p_par[2] = {0, 0};
+        int kt = 0, nt[2] = {0, 0};  // the step: key tile, key tiles of the item per query tile (0: not there)
+        bool more = walk.next(it);
+        int nkt = 0, nnt[2] = {0, 0};  // the next step
+        if (more) {
+            nnt[0] = key_tiles(it, 0, kTok);
+            nnt[1] = key_tiles(it, 1, kTok);
+            nkt = max(nnt[0], nnt[1]) - 1;
         }
-        if (ok) commit(bar(B_FREE));
-        for (int j = 0; j < nt && ok; j++) {
-            const int vi = 2 * j + 1, ki = 2 * j + 2;
-            ok = arrived(vi) && (j > 0 || !fix || wait(bar(B_FIX), 0, &abort_flag, a.status));
-            for (int t = 0; t < 2 && ok; t++) {
-                ok = wait(bar(B_P + t), j & 1, &abort_flag, a.status);
-                if (!ok) break;
+        bool have = false;
+        while (have || more) {
+            if (have) lwait(B_KV + vsl.slot, vsl.par);
+            if (more) lwait(B_KV + ksl.slot, ksl.par);
+#pragma unroll
+            for (int t = 0; t < 2; t++) {
+                const bool do_pv = kt < nt[t], do_qk = nkt < nnt[t];
+                if (do_qk && nkt == nnt[t] - 1) {  // its first key tile
+                    lwait(B_Q + t, q_par[t]);
+                    q_par[t] ^= 1u;
+                }
+                if (do_pv) {
+                    if (kHalves) {
+                        lwait(B_P + 2 * t, p_par[t]);
+                        fence_after();
+                        if (leader) pv(t, vsl.slot, 0, kt < nt[t] - 1);
+                        __syncwarp();
+                    }
+                    lwait(B_P + 2 * t + 1, p_par[t]);
+                    p_par[t] ^= 1u;
+                }
                 fence_after();
-                pv(t, vi % kSlots, j > 0);
-                if (j + 1 == nt) {
-                    commit(bar(B_O + t));
-                } else {
-                    ok = arrived(ki);
-                    if (!ok) break;
-                    qk(t, ki % kSlots);
-                    commit(bar(B_S + t));
-                }
-            }
-            if (!ok) break;
-            commit(bar(B_FREE + vi % kSlots));
-            if (j + 1 < nt) commit(bar(B_FREE + ki % kSlots));
-        }
-        commit(bar(B_END));
-        wait_teardown(bar(B_END), 0);
-    } else if (warp == kWarpFix && fix) {
-        // --------------------------- zero V behind the end of the sequence ----
-        if (warp_wait(bar(B_KV + 1), 0, &abort_flag, a.status)) {
-            const int r0 = it.n - (nt - 1) * kKeys;  // first row of the tile behind the end
-            for (int i = lane; i < (kKeys - r0) * 16; i += 32) {
-                const uint32_t at = ring + kTileBytes + (uint32_t)((i & 1) * kHalfBytes + r0 * 128 + (i >> 1) * 16);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_FIX));
-        }
-    } else if (warp < 8) {
-        // --------------------------------------------------------- softmax ----
-        const int t = warp >> 2, r = tid & 127;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-        const uint32_t s_col = tmem + lanes + kColS + 128 * t, o_col = tmem + lanes + kColO + 128 * t;
-        const int tok = it.m0 + t * kTok + r / G, head = r % G;
-        const bool stored = r < kTok * G && tok < it.n;
-        const int limit = r < kTok * G ? min(tok, it.n - 1) : -1;  // last visible key
-        const float scale2 = kLog2e * 0.08838834764831845f;        // log2(e) / sqrt(128)
-        float m = -INFINITY;
-        uint64_t l[2] = {0ull, 0ull};  // four partial sums
-        bool ok = true;
-        for (int j = 0; j < nt; j++) {
-            if (!warp_wait(bar(B_S + t), j & 1, &abort_flag, a.status)) {
-                ok = false;
-                break;
-            }
-            fence_after();
-            const int lim = limit - (nt - 1 - j) * kKeys;
-            const bool masked = __any_sync(0xffffffffu, lim < kKeys - 1);
-            uint32_t ua[32], ub[32];
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 2; c >= 0; c -= 2) {
-                tmem_ld32(s_col + 32 * c, ua);
-                tmem_ld32(s_col + 32 * c + 32, ub);
-                wait_ld();
-                tie32(ua);
-                tie32(ub);
-                if (masked) {
-                    hide(ua, lim - 32 * c);
-                    hide(ub, lim - 32 * c - 32);
-                }
-                row_max(ua, mx);
-                row_max(ub, mx);
-            }
-            const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale2;
-            const bool grow = top > m + kMargin;
-            if (__any_sync(0xffffffffu, grow)) {
-                const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
-                if (grow) m = top;
-                l[0] = fma2(l[0], pair(f, f), 0ull);
-                l[1] = fma2(l[1], pair(f, f), 0ull);
-                if (j > 0) {  // every product into O so far is complete (it was issued before this S)
-#pragma unroll 1
-                    for (int c = 0; c < 4; c++) {
-                        uint32_t o[32];
-                        tmem_ld32(o_col + 32 * c, o);
-                        wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 32; i++) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                        tmem_st32(o_col + 32 * c, o);
+                if (leader) {
+                    if (do_pv) {
+                        if (!kHalves) pv(t, vsl.slot, 0, kt < nt[t] - 1);
+                        pv(t, vsl.slot, 1, true);
+                        if (kt == 0) commit(bar(B_O + t));
+                    }
+                    if (do_qk) {
+                        qk(t, ksl.slot);
+                        commit(bar(B_S + t));
+                        if (nkt == 0) commit(bar(B_QFREE + t));
+                    }
+                    if (t == 1) {
+                        if (have) commit(bar(B_FREE + vsl.slot));
+                        if (more) commit(bar(B_FREE + ksl.slot));
                     }
                 }
+                __syncwarp();
             }
-            const float ms = m == -INFINITY ? 0.f : -m;
-            const uint64_t scale_2 = pair(scale2, scale2), ms_2 = pair(ms, ms);
-            // hidden keys have to come out as 0 and not as 2^-126: a masked tile takes the exact path
-            if (masked) {
-                weights_row<0>(ua, ub, lim, scale_2, ms_2, l, s_col);
-            } else {
-                weights_row<kPoly>(ua, ub, lim, scale_2, ms_2, l, s_col);
+            // the next step becomes this one
+            have = more;
+            kt = nkt;
+            nt[0] = nnt[0];
+            nt[1] = nnt[1];
+            vsl = ksl;
+            vsl.next();
+            ksl = vsl;
+            ksl.next();
+            if (more && --nkt < 0) {
+                walk.done(lane);
+                more = walk.next(it);
+                nnt[0] = more ? key_tiles(it, 0, kTok) : 0;
+                nnt[1] = more ? key_tiles(it, 1, kTok) : 0;
+                nkt = max(nnt[0], nnt[1]) - 1;
+                if (!more) nkt = 0;
             }
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_P + t));
         }
-        if (ok && warp_wait(bar(B_O + t), 0, &abort_flag, a.status)) {
-            fence_after();
+        if (leader) commit(bar(B_END));
+        __syncwarp();
+        wait_teardown(bar(B_END), 0);
+    } else if (warp == kWarpFix) {
+        // ----------------------------- zero V behind the end of the sequence ----
+        int tile = 0, n_fix = 0;  // running number of the item's first tile in the ring; such items so far
+        while (walk.next(it)) {
+            const int nt = max(key_tiles(it, 0, kTok), key_tiles(it, 1, kTok));
+            if (nt * kKeys > it.n) {
+                const int slot = (tile + 1) % kSlots, r0 = it.n - (nt - 1) * kKeys;  // first row behind the end
+                if (!wwait(B_FIX + n_fix % kFixes, (n_fix / kFixes) & 1)) break;
+                for (int i = lane; i < (kKeys - r0) * 16; i += 32)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                     ring + (uint32_t)(slot * kTileBytes + (i & 1) * kHalfBytes + r0 * 128 + (i >> 1) * 16)),
+                                 "r"(0)
+                                 : "memory");
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_KV + slot));
+                n_fix++;
+            }
+            tile = (tile + 2 * nt) % kSlots;
+            walk.done(lane);
+        }
+    } else {
+        // --------------------------------------------------------- softmax ----
+        const int t = warp >> 2, r = tid & 127, head = r % G;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+        const uint32_t s_col = tmem + lanes + kColS + 128 * t, o_col = tmem + lanes + kColO + 128 * t;
+        uint32_t par = 0, o_par = 0;  // parities of the tile's steps and items
+        while (walk.next(it)) {
+            const int nt = key_tiles(it, t, kTok);
+            const int tok = it.m0 + t * kTok + r / G;
+            const bool stored = r < kTok * G && tok < it.n;
+            const int limit = min(tok, it.n - 1);  // last visible key
             const size_t row = (size_t)(it.row0 + tok) * a.s.Hq + (size_t)it.kvh * G + head;
+            walk.done(lane);
+            if (nt == 0) continue;
+            float m = -INFINITY;
+            uint64_t l[2] = {0ull, 0ull};  // four partial sums
+            bool ok = true;
+            for (int kt = nt - 1; kt >= 0 && ok; kt--, par ^= 1u) {
+                ok = wwait(B_S + t, par);
+                if (!ok) break;
+                fence_after();
+                const int lim = limit - kt * kKeys;
+                const bool masked = __any_sync(0xffffffffu, lim < kKeys - 1);
+                row_tile(m, l, lim, masked, kt < nt - 1, s_col, o_col, bar(B_P + 2 * t), lane);
+            }
+            if (!ok || !wwait(B_O + t, o_par)) break;
+            o_par ^= 1u;
+            fence_after();
             float l0, l1;
             unpair(add2(l[0], l[1]), l0, l1);
             const float sum = l0 + l1, inv = 1.f / sum;
             uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * kHeadDim);
-            uint32_t o[128];
 #pragma unroll
-            for (int c = 0; c < 4; c++) tmem_ld32(o_col + 32 * c, o + 32 * c);
-            wait_ld();
-            if (stored) {
+            for (int c = 0; c < 2; c++) {
+                uint32_t o[64];
+                tmem_ld32(o_col + 64 * c, o);
+                tmem_ld32(o_col + 64 * c + 32, o + 32);
+                wait_ld();
+                tie32(o);
+                tie32(o + 32);
+                if (stored) {
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    uint32_t v[4];
+                    for (int i = 0; i < 8; i++) {
+                        uint32_t v[4];
 #pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        v[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                    dst[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                        for (int k = 0; k < 4; k++)
+                            v[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                        dst[8 * c + i] = make_uint4(v[0], v[1], v[2], v[3]);
+                    }
                 }
+                __syncwarp();
             }
             if (stored && a.lse) a.lse[row] = (m + log2f(sum)) * kLn2;
         }
@@ -603,7 +823,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kWarpTmem) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+    if (warp == kWarpItems)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_sh), "r"(512));
 }
 
 // [rows][heads][128] view with rows `stride` elements apart; a box is 64
@@ -630,8 +851,8 @@ static cudaError_t launch_g(const PromptShape &s, const uint16_t *q, const uint1
     const void *fn = reinterpret_cast<const void *>(prompt_attend_kernel<G>);
     cudaError_t e = ensure_smem(fn, kSmemBytes);
     if (e != cudaSuccess) return e;
-    a.n_items = (int)items;
-    return launch_pdl(prompt_attend_kernel<G>, dim3((unsigned)items), dim3(kThreads), kSmemBytes, st, mq, mk, mv, a);
+    static const int kSms = 148;
+    return launch_pdl(prompt_attend_kernel<G>, dim3((unsigned)(items < kSms ? items : kSms)), dim3(kThreads), kSmemBytes, st, mq, mk, mv, a);
 }
 
 }  // namespace prompt
@@ -646,7 +867,6 @@ cudaError_t launch_prompt(const PromptShape &s, const uint16_t *q, const uint16_
     a.out = out;
     a.lse = lse;
     a.status = status;
-    a.n_items = 0;
     switch (s.G) {
     case 1: return prompt::launch_g<1>(s, q, k, v, a, st);
     case 2: return prompt::launch_g<2>(s, q, k, v, a, st);
