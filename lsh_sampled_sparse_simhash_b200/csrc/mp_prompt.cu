@@ -39,21 +39,14 @@ constexpr int kRows = 128;                    // rows of a query tile = TMEM lan
 constexpr int kKeys = 128;                    // keys of a tile
 constexpr int kHalfBytes = 128 * 128;         // 128 rows x 64 elements
 constexpr int kTileBytes = 2 * kHalfBytes;    // 32 KB
-constexpr int kSlots = 5;                     // ring of K and V tiles
+constexpr int kSlots = 4;                     // ring of K and V tiles
+constexpr int kStageBytes = 4096;             // a softmax warp's stage for results: 32 rows x 64 dims
 constexpr int kItems = 4;                     // items known ahead
 constexpr int kFixes = 4;                     // more than the V tiles that the ring can hold
-constexpr int kSmemBytes = 1024 + (2 + kSlots) * kTileBytes;
+constexpr int kSmemBytes = 1024 + (2 + kSlots) * kTileBytes + 8 * kStageBytes;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpFix = 10, kWarpItems = 11;
 constexpr int kThreads = 32 * 12;
 constexpr uint32_t kColS = 0, kColO = 256;    // + 128 t
-#ifndef KPOLY
-#define KPOLY 2
-#endif
-constexpr int kPoly = KPOLY;                      // of 8 pairs of weights, those computed by polynomial
-#ifndef HALVES
-#define HALVES 1
-#endif
-constexpr bool kHalves = HALVES;
 constexpr float kMargin = 24.f;               // log2 units that a score may exceed its row's reference by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -245,44 +238,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// 2^x of a pair on the multiply-add pipe, x <= 126.  x = n + f with n whole
-// and |f| <= 1/2 (adding and taking away 1.5 2^23 rounds to whole numbers),
-// 2^f by a polynomial, n added to the exponent.  The coefficients minimise the
-// largest relative error on [-1/2, 1/2] among those with value 1 at 0 (fitted
-// by Lawson's iteration): 2.9e-6 = 2^-18.4.  Below -126 the result is between
-// 0 and 2^-126, from -127 on exactly 0 (the 1 at 0 loses its whole exponent).
-// In three parts, so that they can be spread between other instructions.
-struct Ex2Poly {
-    uint64_t t, f, p;
-    __device__ __forceinline__ void split(uint64_t x2)
-    {
-        float x0, x1;
-        unpair(x2, x0, x1);
-        asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x0));  // -127
-        asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x1));
-        const uint64_t x = pair(x0, x1);
-        t = add2(x, pair(12582912.f, 12582912.f));
-        f = add2(x, fma2(t, pair(-1.f, -1.f), pair(12582912.f, 12582912.f)));
-    }
-    __device__ __forceinline__ void first()
-    {
-        p = fma2(f, pair(0.009582852944731712f, 0.009582852944731712f), pair(0.055906426161527634f, 0.055906426161527634f));
-        p = fma2(p, f, pair(0.24024099111557007f, 0.24024099111557007f));
-    }
-    __device__ __forceinline__ void second()
-    {
-        p = fma2(p, f, pair(0.6931241750717163f, 0.6931241750717163f));
-        p = fma2(p, f, pair(1.f, 1.f));
-    }
-    __device__ __forceinline__ void join(float &y0, float &y1) const
-    {
-        float t0, t1, p0, p1;
-        unpair(t, t0, t1);
-        unpair(p, p0, p1);
-        y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
-        y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
-    }
-};
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
 {
     uint32_t r;
@@ -309,27 +264,16 @@ __device__ __forceinline__ void row_max(const uint32_t *u, float *mx)
 }
 
 // The weights of 32 keys of a row, 2^(s scale + ms), as bf16 into 16 columns
-// at p_col, their sums (of the unrounded values) into l.  NPOLY of every 8
-// pairs go by Ex2Poly, the others by the special function unit.
-template <int NPOLY>
+// at p_col, their sums (of the unrounded values) into l.
 __device__ __forceinline__ void weights(const uint32_t *u, uint64_t scale2, uint64_t ms, uint64_t *l, uint32_t p_col)
 {
     uint32_t p[16];
 #pragma unroll
     for (int i = 0; i < 16; i++) {
-        const uint64_t x = fma2(pair(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), scale2, ms);
         float e0, e1;
-        if ((i * NPOLY) % 8 < NPOLY) {
-            Ex2Poly poly;
-            poly.split(x);
-            poly.first();
-            poly.second();
-            poly.join(e0, e1);
-        } else {
-            unpair(x, e0, e1);
-            e0 = ex2(e0);
-            e1 = ex2(e1);
-        }
+        unpair(fma2(pair(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])), scale2, ms), e0, e1);
+        e0 = ex2(e0);
+        e1 = ex2(e1);
         l[i & 1] = add2(l[i & 1], pair(e0, e1));
         p[i] = pack_bf16(e0, e1);
     }
@@ -397,18 +341,18 @@ __device__ __forceinline__ void row_tile(float &m, uint64_t *l, int lim, bool ma
     const float neg = m == -INFINITY ? 0.f : -m;
     const uint64_t scale2 = pair(scale, scale), ms = pair(neg, neg);
     tmem_ld32(s_col + 64, c);
-    weights<kPoly>(a, scale2, ms, l, s_col);
-    weights<kPoly>(b, scale2, ms, l, s_col + 16);
-    if (kHalves) publish(p_bar, lane);
+    weights(a, scale2, ms, l, s_col);
+    weights(b, scale2, ms, l, s_col + 16);
+    publish(p_bar, lane);
     wait_ld();
     tie32(c);
     if (masked) hide(c, lim - 64);
     tmem_ld32(s_col + 96, a);
-    weights<kPoly>(c, scale2, ms, l, s_col + 32);
+    weights(c, scale2, ms, l, s_col + 32);
     wait_ld();
     tie32(a);
     if (masked) hide(a, lim - 96);
-    weights<kPoly>(a, scale2, ms, l, s_col + 48);
+    weights(a, scale2, ms, l, s_col + 48);
     publish(p_bar + 8, lane);
 }
 
@@ -695,19 +639,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     q_par[t] ^= 1u;
                 }
                 if (do_pv) {
-                    if (kHalves) {
-                        lwait(B_P + 2 * t, p_par[t]);
-                        fence_after();
-                        if (leader) pv(t, vsl.slot, 0, kt < nt[t] - 1);
-                        __syncwarp();
-                    }
+                    lwait(B_P + 2 * t, p_par[t]);
+                    fence_after();
+                    if (leader) pv(t, vsl.slot, 0, kt < nt[t] - 1);
+                    __syncwarp();
                     lwait(B_P + 2 * t + 1, p_par[t]);
                     p_par[t] ^= 1u;
                 }
                 fence_after();
                 if (leader) {
                     if (do_pv) {
-                        if (!kHalves) pv(t, vsl.slot, 0, kt < nt[t] - 1);
                         pv(t, vsl.slot, 1, true);
                         if (kt == 0) commit(bar(B_O + t));
                     }
@@ -796,7 +737,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             float l0, l1;
             unpair(add2(l[0], l[1]), l0, l1);
             const float sum = l0 + l1, inv = 1.f / sum;
-            uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * kHeadDim);
+            // 64 dims at a time through the warp's stage, so that a warp's store covers
+            // four whole 128-byte lines and not 16 bytes of 32 (packed prompts 200 -> KK us)
+            const uint32_t stage = ring + kSlots * kTileBytes + warp * kStageBytes;
+            const size_t out0 = (size_t)(it.row0 + it.m0 + t * kTok) * a.s.Hq + (size_t)it.kvh * G;  // the tile's first row
+            const int rows = min(kTok, it.n - it.m0 - t * kTok) * G;  // rows of the tile that exist
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 uint32_t o[64];
@@ -805,14 +750,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait_ld();
                 tie32(o);
                 tie32(o + 32);
-                if (stored) {
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        uint32_t v[4];
+                for (int i = 0; i < 8; i++) {
+                    uint32_t v[4];
 #pragma unroll
-                        for (int k = 0; k < 4; k++)
-                            v[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
-                        dst[8 * c + i] = make_uint4(v[0], v[1], v[2], v[3]);
+                    for (int k = 0; k < 4; k++)
+                        v[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * inv, __uint_as_float(o[8 * i + 2 * k + 1]) * inv);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(stage + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                                 "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+                                 : "memory");
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int lr = 4 * i + (lane >> 3), rr = (warp & 3) * 32 + lr;  // row of the warp, of the tile
+                    uint32_t v[4];
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                 : "r"(stage + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4))
+                                 : "memory");
+                    if (rr < rows) {
+                        const size_t at = out0 + (size_t)(rr / G) * a.s.Hq + rr % G;
+                        reinterpret_cast<uint4 *>(a.out + at * kHeadDim)[8 * c + (lane & 7)] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
                 __syncwarp();
