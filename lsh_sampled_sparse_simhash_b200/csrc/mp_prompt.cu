@@ -708,18 +708,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // --------------------------------------------------------- softmax ----
-        const int t = warp >> 2, r = tid & 127, head = r % G;
+        const int t = warp >> 2, r = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         const uint32_t s_col = tmem + lanes + kColS + 128 * t, o_col = tmem + lanes + kColO + 128 * t;
         uint32_t par = 0, o_par = 0;  // parities of the tile's steps and items
-        while (walk.next(it)) {
+        bool live = walk.next(it);
+        while (live) {
             const int nt = key_tiles(it, t, kTok);
-            const int tok = it.m0 + t * kTok + r / G;
-            const bool stored = r < kTok * G && tok < it.n;
-            const int limit = min(tok, it.n - 1);  // last visible key
-            const size_t row = (size_t)(it.row0 + tok) * a.s.Hq + (size_t)it.kvh * G + head;
+            const int limit = min(it.m0 + t * kTok + r / G, it.n - 1);  // last visible key
+            const size_t out0 = (size_t)(it.row0 + it.m0 + t * kTok) * a.s.Hq + (size_t)it.kvh * G;  // the tile's first row
+            const int rows = min(kTok, it.n - it.m0 - t * kTok) * G;  // rows of the tile that exist
             walk.done(lane);
-            if (nt == 0) continue;
+            if (nt == 0) {
+                live = walk.next(it);
+                continue;
+            }
             float m = -INFINITY;
             uint64_t l[2] = {0ull, 0ull};  // four partial sums
             bool ok = true;
@@ -731,17 +734,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool masked = __any_sync(0xffffffffu, lim < kKeys - 1);
                 row_tile(m, l, lim, masked, kt < nt - 1, s_col, o_col, bar(B_P + 2 * t), lane);
             }
-            if (!ok || !wwait(B_O + t, o_par)) break;
+            if (!ok) break;
+            live = walk.next(it);  // while the last product runs
+            if (!wwait(B_O + t, o_par)) break;
             o_par ^= 1u;
             fence_after();
             float l0, l1;
             unpair(add2(l[0], l[1]), l0, l1);
             const float sum = l0 + l1, inv = 1.f / sum;
             // 64 dims at a time through the warp's stage, so that a warp's store covers
-            // four whole 128-byte lines and not 16 bytes of 32 (packed prompts 200 -> KK us)
+            // four whole 128-byte lines and not 16 bytes of 32 (packed prompts 200 -> 184 us)
             const uint32_t stage = ring + kSlots * kTileBytes + warp * kStageBytes;
-            const size_t out0 = (size_t)(it.row0 + it.m0 + t * kTok) * a.s.Hq + (size_t)it.kvh * G;  // the tile's first row
-            const int rows = min(kTok, it.n - it.m0 - t * kTok) * G;  // rows of the tile that exist
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 uint32_t o[64];
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (stored && a.lse) a.lse[row] = (m + log2f(sum)) * kLn2;
+            if (a.lse && r < rows) a.lse[out0 + (size_t)(r / G) * a.s.Hq + r % G] = (m + log2f(sum)) * kLn2;
         }
     }
     fence_before();
