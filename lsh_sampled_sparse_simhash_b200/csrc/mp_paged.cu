@@ -36,7 +36,9 @@ constexpr int kBlockTok = kWarps * kTile;    // tokens of a block of the split
 constexpr int kStages = 3;
 constexpr int kRowBytes = 256;
 constexpr int kTileBytes = 2 * kTile * kRowBytes;        // K rows, then V rows
-constexpr int kRingBytes = kWarps * kStages * kTileBytes; // 96 KB: two thread blocks per SM
+constexpr int kRingBytes = kWarps * kStages * kTileBytes; // 96 KB
+constexpr int kAccBytes = kWarps * 8 * kHeadDim * 4;      // the warps' sums, where they are joined
+constexpr int kSmemBytes = kRingBytes + kAccBytes;        // 112 KB: two thread blocks per SM
 constexpr int kBlocksPerSm = 2;
 constexpr int kMergeWarps = 4, kMergeBatch = 4;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -126,6 +128,28 @@ __device__ __forceinline__ void fold(float &m, float &l, float4 &v, float m2, fl
     m = mn;
 }
 
+// A walk over a run of the line, block by block: unit after unit, the kv heads
+// of a sequence side by side, sequences without tokens passed over.
+struct Walk {
+    long long left;  // blocks of the run from here on
+    int b, kvh, blk, len, nb;
+    __device__ __forceinline__ void next(const Args &a)
+    {
+        left--;
+        if (++blk < nb || left <= 0) return;
+        blk = 0;
+        if (++kvh < a.s.Hkv) return;
+        kvh = 0;
+        do {
+            len = clamped_len(a, ++b);
+            nb = blocks_of(len);
+        } while (nb == 0);
+    }
+};
+
+// ALIGNED: pages are whole tiles (page_size % 16 == 0), so a tile lies in one
+// page and its table entry is read once, not per row.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel(const Args a)
 {
     extern __shared__ __align__(128) uint8_t ring[];
@@ -139,50 +163,106 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     grid_dependency_wait();
 
     // this thread block's run of the line
-    const long long seq_blocks = blocks_before(a, s.B, lane);
-    const long long W = seq_blocks * s.Hkv;
+    const long long W = blocks_before(a, s.B, lane) * s.Hkv;
     const int c = blockIdx.x, C = live_runs(W, a.C);
     if (c == 0)
         for (int j = tid; j < s.B; j += blockDim.x)
             if (a.lens[j] > a.max_len || a.lens[j] < 0) set_status(a.status, MP_ERR_CAPACITY);
     if (c >= C) return;
-    long long x = c * W / C;
-    const long long x_end = (c + 1) * W / C;
+    const long long x = c * W / C;
     // the sequence that x falls into: 32 sequences a step
-    int b = 0;
-    long long first = 0;  // the line's position of sequence b
-    for (int b0 = 0;; b0 += 32) {
-        const int bb = b0 + lane;
-        const long long n = bb < s.B ? (long long)blocks_of(clamped_len(a, bb)) * s.Hkv : 0;
-        long long pre = n;
+    Walk rd;  // what is read next
+    rd.left = (c + 1) * W / C - x;
+    {
+        long long first = 0;  // the line's position of the step's first sequence
+        for (int b0 = 0;; b0 += 32) {
+            const int bb = b0 + lane;
+            const long long n = bb < s.B ? (long long)blocks_of(clamped_len(a, bb)) * s.Hkv : 0;
+            long long pre = n;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, pre, o);
-            if (lane >= o) pre += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+                if (lane >= o) pre += y;
+            }
+            const unsigned over = __ballot_sync(0xffffffffu, first + pre > x);
+            if (over) {
+                const int l = __ffs((int)over) - 1;
+                rd.b = b0 + l;
+                first += __shfl_sync(0xffffffffu, pre - n, l);
+                break;
+            }
+            first += __shfl_sync(0xffffffffu, pre, 31);
         }
-        const unsigned over = __ballot_sync(0xffffffffu, first + pre > x);
-        if (over) {
-            const int l = __ffs((int)over) - 1;
-            b = b0 + l;
-            first += __shfl_sync(0xffffffffu, pre - n, l);
-            break;
-        }
-        first += __shfl_sync(0xffffffffu, pre, 31);
+        rd.len = clamped_len(a, rd.b);
+        rd.nb = blocks_of(rd.len);
+        rd.kvh = (int)((x - first) / rd.nb);
+        rd.blk = (int)((x - first) % rd.nb);
     }
+    Walk at = rd;  // what is computed next, kStages - 1 blocks behind
 
     const uint32_t my_ring = smem_u32(ring) + (uint32_t)(warp * kStages * kTileBytes);
-    while (x < x_end) {
-        const int len = clamped_len(a, b), nb = blocks_of(len);
-        if (nb == 0) {
-            b++;
-            continue;
-        }
-        const int kvh = (int)((x - first) / nb);
-        const int blk0 = (int)((x - first) % nb);
-        const int blk1 = (int)min((long long)nb, blk0 + (x_end - x));
-        const int32_t *row = a.table + (size_t)b * s.M;
-        const int hq0 = kvh * s.G;
+    float *acc_sh = reinterpret_cast<float *>(ring + kRingBytes);  // [warp][8 heads][128], columns swizzled by head
+    auto acc_at = [&](int w, int h, int d) -> float & { return acc_sh[(w * 8 + h) * kHeadDim + (d ^ ((h >> 1) << 3))]; };
 
+    // The table entry of the next tile is fetched a tile ahead of its copies:
+    // lane i < 16 holds that of token i (ALIGNED: all lanes the tile's one).
+    int tok0 = 0, page = -1;
+    auto fetch = [&]() {
+        if (rd.left <= 0) return;
+        tok0 = (rd.blk * kWarps + warp) * kTile;
+        const int tok = ALIGNED ? tok0 : tok0 + (lane & 15);
+        page = tok < rd.len ? a.table[(size_t)rd.b * s.M + tok / s.S] : -2;
+        if (rd.blk == 0 && lane < 2 * s.G)  // a unit begins: its queries (2 lines a head) into L1
+            asm volatile("prefetch.global.L1 [%0];" ::"l"(
+                a.q + ((size_t)rd.b * s.Hq + rd.kvh * s.G) * kHeadDim + lane * 64));
+    };
+    int slot_rd = 0;
+    auto issue = [&]() {
+        if (rd.left > 0) {
+            const uint32_t dst = my_ring + (uint32_t)(slot_rd * kTileBytes);
+            const bool good = page >= 0 && page < s.P;
+            if (!good && page != -2) set_status(a.status, MP_ERR_CAPACITY);
+            const int p = lane & 15, r0 = lane >> 4;
+            unsigned seen;
+            if (ALIGNED) {
+                const int n = good ? min(rd.len - tok0, kTile) : 0;  // rows that count
+                seen = (1u << max(n, 0)) - 1u;
+                const size_t off = (((size_t)max(page, 0) * s.Hkv + rd.kvh) * s.S + tok0 % s.S + r0) * kHeadDim + p * 8;
+                const uint16_t *k0 = a.kp + (good ? off : 0), *v0 = a.vp + (good ? off : 0);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int r = 2 * i + r0, bytes = r < n ? 16 : 0;  // a row that does not count is zeros: 0 times anything else may be NaN
+                    const size_t o = r < n ? (size_t)(2 * i) * kHeadDim : 0;
+                    cp_async_16_s(dst + row_off(r, p), k0 + o, bytes);
+                    cp_async_16_s(dst + kTile * kRowBytes + row_off(r, p), v0 + o, bytes);
+                }
+            } else {
+                // lanes 0..15: the row of token tok0 + lane in the pools (-1: none)
+                const long long row = good ? ((long long)page * s.Hkv + rd.kvh) * s.S + (tok0 + p) % s.S : -1;
+                seen = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const int r = 2 * i + r0;
+                    const long long ar = __shfl_sync(0xffffffffu, row, r);
+                    const size_t off = (size_t)max(ar, 0ll) * kHeadDim + p * 8;
+                    const int bytes = ar >= 0 ? 16 : 0;
+                    cp_async_16_s(dst + row_off(r, p), a.kp + off, bytes);
+                    cp_async_16_s(dst + kTile * kRowBytes + row_off(r, p), a.vp + off, bytes);
+                }
+            }
+            if (lane == 0) seen_sh[warp][slot_rd] = seen;
+            rd.next(a);
+            fetch();
+        }
+        cp_async_commit();
+        slot_rd = slot_rd == kStages - 1 ? 0 : slot_rd + 1;
+    };
+    fetch();
+    for (int t = 0; t < kStages - 1; t++) issue();
+
+    int slot = 0;
+    while (at.left > 0) {
+        const int hq0 = at.kvh * s.G, b = at.b, nb = at.nb, blk0 = at.blk;
         // query fragments: B of m16n8k16 (k = dims, n = heads), zero for heads past G
         uint32_t qf[8][2];
 #pragma unroll
@@ -190,49 +270,22 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
 #pragma unroll
             for (int j = 0; j < 2; j++) {
                 const uint16_t *qr = a.q + ((size_t)b * s.Hq + hq0 + g4) * kHeadDim + ks * 16 + j * 8 + t4 * 2;
-                qf[ks][j] = g4 < s.G ? *reinterpret_cast<const uint32_t *>(qr) : 0u;
+                qf[ks][j] = g4 < s.G ? __ldg(reinterpret_cast<const uint32_t *>(qr)) : 0u;
             }
-
-        // tiles of this warp: tokens (blk0 * 4 + warp + 4 t) * 16
-        const int nt = blk1 - blk0;
-        auto issue = [&](int t) {
-            if (t < nt) {
-                const int tok0 = ((blk0 + t) * kWarps + warp) * kTile;
-                const uint32_t dst = my_ring + (uint32_t)((t % kStages) * kTileBytes);
-                // lanes 0..15: the row of token tok0 + lane in the pools (-1: none)
-                long long at = -1;
-                const int tok = tok0 + (lane & 15);
-                if (tok < len) {
-                    const int page = row[tok / s.S];
-                    if (page >= 0 && page < s.P) at = ((long long)page * s.Hkv + kvh) * s.S + tok % s.S;
-                    else set_status(a.status, MP_ERR_CAPACITY);
-                }
-                const unsigned seen = __ballot_sync(0xffffffffu, at >= 0) & 0xffffu;
-#pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int r = 2 * i + (lane >> 4), p = lane & 15;
-                    const long long ar = __shfl_sync(0xffffffffu, at, r);
-                    const size_t off = (size_t)max(ar, 0ll) * kHeadDim + p * 8;
-                    const int n = ar >= 0 ? 16 : 0;  // a row that does not count is zeros: 0 times anything else may be NaN
-                    cp_async_16_s(dst + row_off(r, p), a.kp + off, n);
-                    cp_async_16_s(dst + kTile * kRowBytes + row_off(r, p), a.vp + off, n);
-                }
-                if (lane == 0) seen_sh[warp][t % kStages] = seen;
-            }
-            cp_async_commit();
-        };
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         float o[8][4];
 #pragma unroll
         for (int i = 0; i < 8; i++)
 #pragma unroll
             for (int j = 0; j < 4; j++) o[i][j] = 0.f;
-        for (int t = 0; t < kStages - 1; t++) issue(t);
+        // the unit's blocks of this run
+        const int nt = (int)min((long long)(nb - blk0), at.left);
         for (int t = 0; t < nt; t++) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            const uint32_t kt = my_ring + (uint32_t)((t % kStages) * kTileBytes), vt = kt + kTile * kRowBytes;
-            const unsigned seen = seen_sh[warp][t % kStages];
+            const uint32_t kt = my_ring + (uint32_t)(slot * kTileBytes), vt = kt + kTile * kRowBytes;
+            const unsigned seen = seen_sh[warp][slot];
+            slot = slot == kStages - 1 ? 0 : slot + 1;
             // S^T: 16 tokens x 8 heads
             float c0 = 0.f, c1 = 0.f, c2 = 0.f, c3 = 0.f;
 #pragma unroll
@@ -300,18 +353,15 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
                 o[i][3] += d3;
             }
             __syncwarp();  // every lane has read the tile before its slot is refilled
-            issue(t + kStages - 1);
+            issue();
+            at.next(a);
         }
-        cp_async_wait<0>();
-        // ---- the warps' states, joined in the ring's memory ----
+        // ---- the warps' states, joined in shared memory (copies of what follows are in flight) ----
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {
             l0 += __shfl_xor_sync(0xffffffffu, l0, w);
             l1 += __shfl_xor_sync(0xffffffffu, l1, w);
         }
-        __syncthreads();
-        float *acc_sh = reinterpret_cast<float *>(ring);  // [warp][8 heads][128 + 4]
-        constexpr int kPitch = kHeadDim + 4;
         if (g4 == 0) {
             red_ml[warp][0][h0] = m0;
             red_ml[warp][0][h1] = m1;
@@ -320,16 +370,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
         }
 #pragma unroll
         for (int i = 0; i < 8; i++) {
-            float *d0 = acc_sh + (warp * 8 + h0) * kPitch + i * 16 + g4;
-            float *d1 = acc_sh + (warp * 8 + h1) * kPitch + i * 16 + g4;
-            d0[0] = o[i][0];
-            d1[0] = o[i][1];
-            d0[8] = o[i][2];
-            d1[8] = o[i][3];
+            acc_at(warp, h0, i * 16 + g4) = o[i][0];
+            acc_at(warp, h1, i * 16 + g4) = o[i][1];
+            acc_at(warp, h0, i * 16 + g4 + 8) = o[i][2];
+            acc_at(warp, h1, i * 16 + g4 + 8) = o[i][3];
         }
         __syncthreads();
-        const bool whole = blk0 == 0 && blk1 == nb;
-        const int slot = c * 2 + (blk0 == 0 ? 1 : 0);
+        const bool whole = blk0 == 0 && nt == nb;
+        const int part = c * 2 + (blk0 == 0 ? 1 : 0);
         for (int h = 0; h < s.G; h++) {  // thread = dim
             float m = -INFINITY;
 #pragma unroll
@@ -339,27 +387,23 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             for (int w = 0; w < kWarps; w++) {
                 const float f = red_ml[w][0][h] == -INFINITY ? 0.f : ex2(red_ml[w][0][h] - m);
                 l += f * red_ml[w][1][h];
-                v += f > 0.f ? f * acc_sh[(w * 8 + h) * kPitch + tid] : 0.f;
+                v += f > 0.f ? f * acc_at(w, h, tid) : 0.f;
             }
             if (whole) {
                 const size_t bh = (size_t)b * s.Hq + hq0 + h;
-                a.out[bh * kHeadDim + tid] = l > 0.f ? v / l : (l == 0.f ? 0.f : v / l);
+                a.out[bh * kHeadDim + tid] = l == 0.f ? 0.f : v / l;
                 if (tid == 0) a.lse[bh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             } else {
-                a.pacc[((size_t)slot * 8 + h) * kHeadDim + tid] = v;
+                a.pacc[((size_t)part * 8 + h) * kHeadDim + tid] = v;
                 if (tid == 0) {
-                    a.pml[((size_t)slot * 8 + h) * 2] = m;
-                    a.pml[((size_t)slot * 8 + h) * 2 + 1] = l;
+                    a.pml[((size_t)part * 8 + h) * 2] = m;
+                    a.pml[((size_t)part * 8 + h) * 2 + 1] = l;
                 }
             }
         }
-        __syncthreads();  // the ring is free again
-        x += blk1 - blk0;
-        if (kvh == s.Hkv - 1 && blk1 == nb) {
-            first += (long long)nb * s.Hkv;
-            b++;
-        }
+        __syncthreads();  // acc_sh and red_ml are free again
     }
+    cp_async_wait<0>();
 }
 
 // Joins the partials of the units that several runs share, and writes the
@@ -454,9 +498,10 @@ cudaError_t launch_paged_attend(const PagesShape &s, const uint16_t *q, const ui
     a.pml = a.pacc + (size_t)a.C * 2 * 8 * kHeadDim;
     a.status = status;
     if (a.C > 0) {
-        cudaError_t e = ensure_smem(reinterpret_cast<const void *>(paged::paged_attend_kernel), paged::kRingBytes);
+        auto kernel = s.S % paged::kTile == 0 ? paged::paged_attend_kernel<true> : paged::paged_attend_kernel<false>;
+        cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), paged::kSmemBytes);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(paged::paged_attend_kernel, dim3(a.C), dim3(32 * paged::kWarps), paged::kRingBytes, st, a);
+        e = launch_pdl(kernel, dim3(a.C), dim3(32 * paged::kWarps), paged::kSmemBytes, st, a);
         if (e != cudaSuccess) return e;
     }
     return launch_pdl(paged::merge_partials_kernel, dim3(s.B * s.Hq), dim3(32 * paged::kMergeWarps), 0, st, a);
