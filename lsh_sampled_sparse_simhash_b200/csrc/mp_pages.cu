@@ -24,7 +24,7 @@ namespace cg = cooperative_groups;
 constexpr int kPlanBlocks = 8;    // portable cluster size
 constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kPlanUnroll = 4;    // 32-page groups in flight per warp
+constexpr int kPlanUnroll = 16;   // 32-page groups in flight per warp
 
 // ---------------------------------------------------------- plan helpers ----
 // The run of pages [lo, hi) of one warp of the cluster; runs are whole groups
@@ -32,9 +32,13 @@ constexpr int kPlanUnroll = 4;    // 32-page groups in flight per warp
 struct PageRun {
     int lo, hi;
 };
+__device__ __forceinline__ int run_groups(int P)
+{
+    return ((P + 31) / 32 + kPlanBlocks * kPlanWarps - 1) / (kPlanBlocks * kPlanWarps);
+}
 __device__ __forceinline__ PageRun page_run(int P, int block, int warp)
 {
-    const int groups = (P + 31) / 32, per = (groups + kPlanBlocks * kPlanWarps - 1) / (kPlanBlocks * kPlanWarps);
+    const int groups = (P + 31) / 32, per = run_groups(P);
     const int g = (block * kPlanWarps + warp) * per;
     PageRun r;
     r.lo = min(g, groups) * 32;
@@ -42,10 +46,13 @@ __device__ __forceinline__ PageRun page_run(int P, int block, int warp)
     return r;
 }
 
-// Used pages (count > 0) of a run.
-__device__ __forceinline__ int count_used(const int32_t *refs, PageRun r, int lane)
+// Used pages (count > 0) of a run.  word: lane g keeps the used bits of the
+// run's g-th group of 32 (the first 32 groups), so that a run of up to 1024
+// pages (a pool of up to 131072) is read once.
+__device__ __forceinline__ int count_used(const int32_t *refs, PageRun r, int lane, uint32_t &word)
 {
-    int n = 0;
+    int n = 0, g = 0;
+    word = 0u;
     for (int p0 = r.lo; p0 < r.hi; p0 += 32 * kPlanUnroll) {
         int v[kPlanUnroll];
 #pragma unroll
@@ -54,33 +61,70 @@ __device__ __forceinline__ int count_used(const int32_t *refs, PageRun r, int la
             v[j] = p < r.hi ? __ldcg(refs + p) : 0;
         }
 #pragma unroll
-        for (int j = 0; j < kPlanUnroll; j++) n += __popc(__ballot_sync(0xffffffffu, v[j] > 0));
+        for (int j = 0; j < kPlanUnroll; j++, g++) {
+            const uint32_t used = __ballot_sync(0xffffffffu, v[j] > 0);
+            n += __popc(used);
+            if (lane == g) word = used;
+        }
     }
     return n;
 }
 
-// Calls f(page, in the run?, count, used pages before it) for the pages of the
+// Calls f(page, in the run?, used?, used pages before it) for the pages of the
 // run, all lanes of a 32-page group together; f returns false (uniformly) to
 // stop.  Pages below `from` are not looked at (used_before covers them).
 template <typename F>
-__device__ __forceinline__ void walk_pages(const int32_t *refs, PageRun r, int from, int used_before, int lane, F f)
+__device__ __forceinline__ void walk_pages(const int32_t *refs, PageRun r, uint32_t word, int from, int used_before, int lane,
+                                           F f)
 {
+    const bool kept = r.hi - r.lo <= 1024;
     int before = used_before;
-    for (int p0 = r.lo; p0 < r.hi; p0 += 32 * kPlanUnroll) {
-        int v[kPlanUnroll];
-#pragma unroll
-        for (int j = 0; j < kPlanUnroll; j++) {
-            const int p = p0 + 32 * j + lane;
-            v[j] = p >= from && p < r.hi ? __ldcg(refs + p) : 0;
-        }
-#pragma unroll
-        for (int j = 0; j < kPlanUnroll; j++) {
-            const int p = p0 + 32 * j + lane;
-            const unsigned used = __ballot_sync(0xffffffffu, v[j] > 0);
-            if (!f(p, p >= from && p < r.hi, v[j], before + __popc(used & ((1u << lane) - 1u)))) return;
-            before += __popc(used);
-        }
+    for (int p0 = r.lo, g = 0; p0 < r.hi; p0 += 32, g++) {
+        const int p = p0 + lane;
+        uint32_t used = kept ? __shfl_sync(0xffffffffu, word, g)
+                             : __ballot_sync(0xffffffffu, p < r.hi && __ldcg(refs + p) > 0);
+        if (p0 < from) used &= from - p0 >= 32 ? 0u : ~0u << (from - p0);
+        if (!f(p, p >= from && p < r.hi, (used >> lane) & 1u, before + __popc(used & ((1u << lane) - 1u)))) return;
+        before += __popc(used);
     }
+}
+
+// Calls f(page, rank) for the free pages with rank < total (rank: free pages
+// before it) of a block's runs, its groups of 32 pages dealt out over its
+// warps: the lowest free pages often lie in the runs of one or two.
+template <typename F>
+__device__ __forceinline__ void take_pages(const int32_t *refs, int P, PageRun r, uint32_t word, int used_before, int total,
+                                           int warp, int lane, F f)
+{
+    __shared__ uint32_t words[kPlanWarps][32];
+    __shared__ int first[kPlanWarps][32], lo[kPlanWarps], kept[kPlanWarps];
+    int pre = __popc(word);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += x;
+    }
+    words[warp][lane] = word;
+    first[warp][lane] = r.lo + 32 * lane - (used_before + pre - __popc(word));  // rank of the group's first free page
+    if (lane == 0) {
+        lo[warp] = r.lo;
+        kept[warp] = r.hi - r.lo <= 1024 ? r.hi : -1;
+    }
+    __syncthreads();
+    const int groups = min(run_groups(P), 32);
+    for (int g = 0; g < groups; g++) {  // another run for every group
+        const int w = (warp + g) % kPlanWarps, p = lo[w] + 32 * g + lane;
+        if (kept[w] < 0 || lo[w] + 32 * g >= kept[w] || first[w][g] >= total) continue;
+        const uint32_t is_free = ~words[w][g];
+        const int k = first[w][g] + __popc(is_free & ((1u << lane) - 1u));
+        if (p < kept[w] && ((is_free >> lane) & 1u) && k < total) f(p, k);
+    }
+    if (r.hi - r.lo > 1024)  // a run too long for its words: walked by its own warp
+        walk_pages(refs, r, word, 0, used_before, lane, [&](int p, bool in, bool used_page, int before) {
+            const int k = p - before;
+            if (in && !used_page && k < total) f(p, k);
+            return __any_sync(0xffffffffu, k < total);
+        });
 }
 
 // Shared state of a plan.
@@ -174,21 +218,27 @@ __device__ __forceinline__ int find_slot(const int *pre, int n, int k)
     return lo;
 }
 
-// Pages that a table row holds: its leading entries >= 0 (33-ary search by
-// a warp, so two or three dependent loads).
+// Pages that a table row holds: its leading entries >= 0.  A 17-ary search by
+// half a warp (so two rows a warp, and three dependent loads for 4000
+// columns); row is null for a half without one.
 __device__ __forceinline__ int held_pages(const int32_t *row, int M, int lane)
 {
-    int lo = 0, hi = M;  // row[lo - 1] >= 0 (or lo = 0), row[hi] < 0 (or hi = M)
-    while (lo < hi) {
-        const int step = (hi - lo + 31) / 32;
-        const int at = lo + step * lane;
+    const int sub = lane & 15, shift = lane & 16;
+    int lo = 0, hi = row ? M : 0;  // row[lo - 1] >= 0 (or lo = 0), row[hi] < 0 (or hi = M)
+    while (__any_sync(0xffffffffu, lo < hi)) {
+        const int step = max((hi - lo + 15) / 16, 1), at = lo + step * sub;
         const bool held = at < hi && __ldcg(row + at) >= 0;
-        const unsigned bal = __ballot_sync(0xffffffffu, held);
-        const int k = bal == 0xffffffffu ? 32 : __ffs((int)~bal) - 1;  // leading probes that hold a page
-        if (k == 0) return lo;
-        const int end = lo + step * k;
-        lo = lo + step * (k - 1) + 1;
-        hi = min(hi, end);
+        const unsigned bal = (__ballot_sync(0xffffffffu, held) >> shift) & 0xffffu;
+        const int k = __ffs((int)~bal) - 1;  // leading probes that hold a page (16: all)
+        if (lo < hi) {
+            if (k == 0) {
+                hi = lo;
+            } else {
+                const int end = lo + step * k;
+                lo += step * (k - 1) + 1;
+                hi = min(hi, end);
+            }
+        }
     }
     return lo;
 }
@@ -205,37 +255,37 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     grid_dependency_wait();
     cl.sync();  // every block of the cluster runs before its shared memory is written from another
     int err = 0;
-    for (int b = blk * kPlanWarps + warp; b < s.B; b += kPlanBlocks * kPlanWarps) {
-        const int n = n_new[b], len = lens[b];
-        const int h = held_pages(table + (size_t)b * s.M, s.M, lane);
+    const PageRun run = page_run(s.P, blk, warp);
+    uint32_t word;
+    const int mine = count_used(refs, run, lane, word);
+    for (int b0 = 2 * (blk * kPlanWarps + warp); b0 < s.B; b0 += 2 * kPlanBlocks * kPlanWarps) {  // two rows a warp
+        const int b = b0 + (lane >> 4);
+        const bool in = b < s.B;
+        const int n = in ? n_new[b] : 0, len = in ? lens[b] : 0;
+        const int h = held_pages(in ? table + (size_t)b * s.M : nullptr, s.M, lane);
         long long want = 0;
         if (n > 0) {
             const long long all = (long long)max(len, 0) + n;
             if (len < 0 || all > (long long)s.M * s.S) err = MP_ERR_CAPACITY;
             else want = max((all + s.S - 1) / s.S - h, 0ll);
         }
-        if (lane < kPlanBlocks) {
-            *cl.map_shared_rank(&need[b], lane) = (int)want;
-            *cl.map_shared_rank(&have[b], lane) = h;
+        if (in && (lane & 15) < kPlanBlocks) {
+            *cl.map_shared_rank(&need[b], lane & 15) = (int)want;
+            *cl.map_shared_rank(&have[b], lane & 15) = h;
         }
     }
-    const PageRun run = page_run(s.P, blk, warp);
     int before, used;
-    err = plan_meet(sh, count_used(refs, run, lane), err, before, used);
+    err = plan_meet(sh, mine, err, before, used);
     const int total = block_exclusive(need, s.B, sh);
     if (total > s.P - used && !err) err = MP_ERR_CAPACITY;
     if (err) {
         if (blk == 0 && threadIdx.x == 0) set_status(status, err);
         return;
     }
-    walk_pages(refs, run, 0, before, lane, [&](int p, bool in, int count, int used_before) {
-        const int k = p - used_before;  // free pages before p
-        if (in && count <= 0 && k < total) {
-            const int b = find_slot(need, s.B, k);
-            table[(size_t)b * s.M + have[b] + (k - need[b])] = p;
-            refs[p] = 1;
-        }
-        return __any_sync(0xffffffffu, k < total);
+    take_pages(refs, s.P, run, word, before, total, warp, lane, [&](int p, int k) {
+        const int b = find_slot(need, s.B, k);
+        table[(size_t)b * s.M + have[b] + (k - need[b])] = p;
+        refs[p] = 1;
     });
 }
 
@@ -257,6 +307,9 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     }
     cl.sync();
     int err = 0;
+    const PageRun run = page_run(s.P, blk, warp);
+    uint32_t word;
+    const int mine = count_used(refs, run, lane, word);
     // every block looks the whole list over
     for (int i = tid; i < n; i += kPlanThreads) {
         const int a = src[i], b = dst[i];
@@ -286,9 +339,8 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
             if (p < 0 || p >= s.P || __ldcg(refs + p) < 1) err = MP_ERR_ARG;
         }
     }
-    const PageRun run = page_run(s.P, blk, warp);
     int before, used;
-    err = plan_meet(sh, count_used(refs, run, lane), err, before, used);
+    err = plan_meet(sh, mine, err, before, used);
     const int total = block_exclusive(need, n, sh);
     if (!err && total > s.P - used) err = MP_ERR_CAPACITY;
     if (blk == 0 && tid == 0) copies[0] = make_int4(err ? 0 : total, 0, 0, 0);
@@ -296,16 +348,12 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         if (blk == 0 && tid == 0) set_status(status, err);
         return;
     }
-    walk_pages(refs, run, 0, before, lane, [&](int p, bool in, int count, int used_before) {
-        const int k = p - used_before;
-        if (in && count <= 0 && k < total) {
-            const int i = find_slot(need, n, k);  // the last fork with k pages before it: the one that takes this page
-            const int a = src[i], len = lens[a], c = len / s.S;
-            table[(size_t)dst[i] * s.M + c] = p;
-            refs[p] = 1;
-            copies[1 + k] = make_int4(table[(size_t)a * s.M + c], p, len % s.S, 0);
-        }
-        return __any_sync(0xffffffffu, k < total);
+    take_pages(refs, s.P, run, word, before, total, warp, lane, [&](int p, int k) {
+        const int i = find_slot(need, n, k);  // the last fork with k pages before it: the one that takes this page
+        const int a = src[i], len = lens[a], c = len / s.S;
+        table[(size_t)dst[i] * s.M + c] = p;
+        refs[p] = 1;
+        copies[1 + k] = make_int4(table[(size_t)a * s.M + c], p, len % s.S, 0);
     });
     for (int i = blk * kPlanWarps + warp; i < n; i += kPlanBlocks * kPlanWarps) {
         const int a = src[i], b = dst[i], len = lens[a], full = len / s.S, keep = full + (len % s.S != 0);
@@ -324,7 +372,9 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
 
 // ------------------------------------------------------------------ free ----
 // One block per entry of the list.  Only the first entry of a sequence acts.
-__global__ void __launch_bounds__(128) pages_free_kernel(PagesShape s, const int32_t *seqs, int32_t *table, int32_t *lens,
+constexpr int kFreeThreads = 256, kFreeBatch = 4;
+
+__global__ void __launch_bounds__(kFreeThreads) pages_free_kernel(PagesShape s, const int32_t *seqs, int32_t *table, int32_t *lens,
                                                          int32_t *refs, int32_t *status)
 {
     grid_dependency_wait();
@@ -337,14 +387,24 @@ __global__ void __launch_bounds__(128) pages_free_kernel(PagesShape s, const int
     for (int j = threadIdx.x; j < i; j += blockDim.x) again |= seqs[j] == b;
     if (__syncthreads_or(again)) return;
     int32_t *row = table + (size_t)b * s.M;
-    for (int c = threadIdx.x; c < s.M; c += blockDim.x) {
-        const int p = row[c];
-        if (p < 0) continue;
-        if (p >= s.P || atomicSub(refs + p, 1) <= 0) {
-            if (p < s.P) atomicAdd(refs + p, 1);
-            set_status(status, MP_ERR_ARG);
+    for (int c0 = 0; c0 < s.M; c0 += kFreeThreads * kFreeBatch) {  // loads, then counts, in batches: both are round trips
+        int p[kFreeBatch], old[kFreeBatch];
+#pragma unroll
+        for (int j = 0; j < kFreeBatch; j++) {
+            const int c = c0 + j * kFreeThreads + threadIdx.x;
+            p[j] = c < s.M ? row[c] : -1;
         }
-        row[c] = -1;
+#pragma unroll
+        for (int j = 0; j < kFreeBatch; j++) old[j] = p[j] >= 0 && p[j] < s.P ? atomicSub(refs + p[j], 1) : 1;
+#pragma unroll
+        for (int j = 0; j < kFreeBatch; j++) {
+            if (p[j] < 0) continue;
+            if (p[j] >= s.P || old[j] <= 0) {
+                if (p[j] < s.P) atomicAdd(refs + p[j], 1);
+                set_status(status, MP_ERR_ARG);
+            }
+            row[c0 + j * kFreeThreads + threadIdx.x] = -1;
+        }
     }
     if (threadIdx.x == 0) lens[b] = 0;
 }
@@ -359,11 +419,13 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     grid_dependency_wait();
     cl.sync();
     const PageRun run = page_run(s.P, blk, warp);
+    uint32_t word;
+    const int mine = count_used(refs, run, lane, word);
     int before, U;
-    plan_meet(sh, count_used(refs, run, lane), 0, before, U);
+    plan_meet(sh, mine, 0, before, U);
     // the i-th free page below U takes move i; whoever meets page U tells all how many used ones are below it
-    walk_pages(refs, run, 0, before, lane, [&](int p, bool in, int count, int used_before) {
-        if (in && p < U && count <= 0) copies[4 * (1 + p - used_before) + 1] = p;
+    walk_pages(refs, run, word, 0, before, lane, [&](int p, bool in, bool used_page, int used_before) {
+        if (in && p < U && !used_page) copies[4 * (1 + p - used_before) + 1] = p;
         if (in && p == U)
             for (int b = 0; b < kPlanBlocks; b++) *cl.map_shared_rank(&sh.lru, b) = used_before;
         return __any_sync(0xffffffffu, in && p <= U);
@@ -376,15 +438,14 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
     }
     if (U == lru) return;  // the same for all blocks
     // the pages from U on move (those below are being given counts meanwhile)
-    const PageRun tail = {max(run.lo, U & ~31), run.hi};
-    walk_pages(refs, tail, U, run.lo > U ? before : lru, lane, [&](int p, bool in, int count, int used_before) {
-        if (in && p >= U && count > 0) {
+    walk_pages(refs, run, word, U, run.lo > U ? before : lru, lane, [&](int p, bool in, bool used_page, int used_before) {
+        if (in && used_page) {
             int32_t *e = copies + 4 * (size_t)(1 + used_before - lru);
             const int to = __ldcg(e + 1);
             e[0] = p;
             e[2] = s.S;
             e[3] = 0;
-            refs[to] = count;
+            refs[to] = __ldcg(refs + p);
             refs[p] = -1 - to;  // where it went, until the table has followed
         }
         return true;
@@ -399,8 +460,8 @@ __global__ void __cluster_dims__(kPlanBlocks, 1, 1) __launch_bounds__(kPlanThrea
         }
     }
     cl.sync();
-    for (int p = tail.lo + lane; p < tail.hi; p += 32)
-        if (p >= U && __ldcg(refs + p) < 0) refs[p] = 0;
+    for (int p = max(run.lo, U) + lane; p < run.hi; p += 32)
+        if (__ldcg(refs + p) < 0) refs[p] = 0;
 }
 
 // ------------------------------------------------------------------ copy ----
@@ -564,7 +625,7 @@ cudaError_t launch_pages_fork(const PagesShape &s, const int32_t *src, const int
 cudaError_t launch_pages_free(const PagesShape &s, const int32_t *seqs, int n, int32_t *table, int32_t *lens,
                               int32_t *refs, int32_t *status, cudaStream_t st)
 {
-    return launch_pdl(pages_free_kernel, dim3(n), dim3(128), 0, st, s, seqs, table, lens, refs, status);
+    return launch_pdl(pages_free_kernel, dim3(n), dim3(kFreeThreads), 0, st, s, seqs, table, lens, refs, status);
 }
 
 cudaError_t launch_pages_compact(const PagesShape &s, int32_t *table, int32_t *refs, int32_t *copies, int32_t *status,
