@@ -317,8 +317,9 @@ int mp_decode_attend_q8(const mp_shape *shape, const void *q, const void *W, con
 
 /*
  * Shape of mp_prompt_attend.  Supported: batch >= 1; head_dim == 128;
- * G in 1 .. 8; 0 <= total < 2^28; strides in elements, multiples of 8 (16
- * bytes), at least n_heads * head_dim.
+ * G in 1 .. 8; 0 <= total < 2^25 (so that no wait inside the kernel comes
+ * near its limit of 1 s); strides in elements, multiples of 8 (16 bytes), at
+ * least n_heads * head_dim.
  */
 typedef struct mp_prompt_shape {
     int32_t batch;      /* B: sequences in the batch */
@@ -392,9 +393,9 @@ int mp_paged_workspace_bytes(const mp_pages_shape *shape, int32_t max_len, size_
  *   max_len  host bound on every seq_lens[b], 0 <= max_len <= M * S (sizes the
  *            grid); a longer sequence is cut there, MP_ERR_CAPACITY recorded
  *   out  fp32 [B][Hq][d]     lse  fp32 [B][Hq]
- *   workspace  device scratch of at least mp_paged_workspace_bytes bytes (16
- *            where that is 0); its contents need not be kept or cleared.  Two
- *            calls that may run at the same time need one each.
+ *   workspace  device scratch of at least mp_paged_workspace_bytes bytes (may
+ *            be null where that is 0); its contents need not be kept or
+ *            cleared.  Two calls that may run at the same time need one each.
  * Rows of a page past the sequence's length may hold anything.  A page number
  * outside [0, P) within a sequence's length: its tokens are left out and
  * MP_ERR_CAPACITY recorded.  Weights keep 24 bits (three bf16 parts) in their

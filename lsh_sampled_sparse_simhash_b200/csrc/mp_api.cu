@@ -73,7 +73,7 @@ int validate_prompt_shape(const mp_prompt_shape *in, PromptShape &s)
     int r = validate_heads(s.Hq, s.Hkv, in->head_dim, s.G);
     if (r) return r;
     if (s.Hq > 65535) return MP_ERR_SHAPE;
-    if (s.B < 1 || s.T < 0 || s.T >= (1 << 28)) return MP_ERR_SHAPE;
+    if (s.B < 1 || s.T < 0 || s.T >= (1 << 25)) return MP_ERR_SHAPE;
     if ((r = token_stride(in->q_stride, s.Hq, s.qs)) || (r = token_stride(in->k_stride, s.Hkv, s.ks)) ||
         (r = token_stride(in->v_stride, s.Hkv, s.vs)))
         return r;
@@ -335,10 +335,12 @@ int mp_paged_attend(const mp_pages_shape *shape, const void *q, const void *k_pa
     PagesShape s;
     int r = validate_pages_shape(shape, s);
     if (r) return r;
-    if ((r = check_ptrs({q, k_pages, v_pages, out, workspace})) || (r = check_words({page_table, seq_lens, lse}))) return r;
+    if ((r = check_ptrs({q, k_pages, v_pages, out})) || (r = check_words({page_table, seq_lens, lse}))) return r;
     if (!aligned4(status)) return MP_ERR_ALIGN;
     if (max_len < 0 || max_len > (int64_t)s.M * s.S) return MP_ERR_CAPACITY;
-    if (workspace_bytes < paged_workspace_bytes(s, max_len)) return MP_ERR_WORKSPACE;
+    const size_t need = paged_workspace_bytes(s, max_len);
+    if (need > 0 && (r = check_ptrs({workspace}))) return r;
+    if (workspace_bytes < need) return MP_ERR_WORKSPACE;
     return cuda_status(launch_paged_attend(s, static_cast<const uint16_t *>(q), static_cast<const uint16_t *>(k_pages),
                                            static_cast<const uint16_t *>(v_pages), page_table, seq_lens, max_len, out, lse,
                                            workspace, status, static_cast<cudaStream_t>(stream)));

@@ -141,6 +141,37 @@ def test_prompt_captured_and_replayed_with_other_lengths():
     check_prompt(q, k, v, cu, out.cpu(), lse.cpu())
 
 
+def test_prompt_two_streams_at_once():
+    """Two calls on two streams, again and again: each waits for the tensor memory that the other holds."""
+    cases = [prompt_case([700 - 300 * j, 45, 300], 8, 2, seed=110 + j) for j in range(2)]
+    runs = []
+    for q, k, v, cu in cases:
+        t = [x.cuda() for x in (q, k, v)]
+        runs.append((t, i32(cu), torch.zeros(q.shape, dtype=torch.bfloat16, device="cuda"),
+                     torch.zeros(q.shape[:2], device="cuda"), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for t, cu, out, lse, st in runs:
+            mp.prompt_attend(mp.PromptShape(3, 8, 2, D, out.shape[0]), *t, cu, out, lse, stream=st)
+    torch.cuda.synchronize()
+    for (q, k, v, cu), (_, _, out, lse, _) in zip(cases, runs):
+        check_prompt(q, k, v, cu, out.cpu(), lse.cpu())
+
+
+def test_prompt_rows_past_32_bits():
+    """A short prompt at the end of row arrays of more than 2^31 elements (and 2^32 bytes)."""
+    lead, n, hq, hkv = 560000, 150, 32, 4
+    assert (lead + n) * hq * D > 1 << 31
+    q, k, v, _ = prompt_case([n], hq, hkv, seed=120)
+    with_lead = [torch.empty(lead + n, x.shape[1], D, dtype=torch.bfloat16, device="cuda") for x in (q, k, v)]
+    for big, x in zip(with_lead, (q, k, v)):
+        big[lead:] = x.cuda()
+    out = torch.empty(lead + n, hq, D, dtype=torch.bfloat16, device="cuda")
+    mp.prompt_attend(mp.PromptShape(1, hq, hkv, D, lead + n), *with_lead, i32([lead, lead + n]), out)
+    check_prompt(q[:, :2], k[:, :1], v[:, :1], [0, n], out[lead:, :2].cpu(), None)
+    check_prompt(q[:, 30:], k[:, 3:], v[:, 3:], [0, n], out[lead:, 30:].cpu(), None)
+
+
 def test_prompt_same_result_every_time():
     q, k, v, cu = prompt_case([333, 20, 512], 8, 2, seed=10)
     a, b = run_prompt(q, k, v, cu), run_prompt(q, k, v, cu)
@@ -230,6 +261,17 @@ def test_paged_few_tokens(lens):
     for max_len in (max(lens), max(16, max(lens))):
         out, lse = run_paged(q, k, v, table, lens, max_len=max_len)
         check_paged(q, k, v, table, lens, out, lse)
+
+
+def test_paged_no_workspace_for_no_tokens():
+    """max_len 0 needs no workspace: an empty tensor (null) does."""
+    q, k, v, table = paged_case([0, 0], 4, 2, 16, seed=55)
+    shape = mp.PagesShape(2, 4, 2, D, k.shape[0], 16, len(table[0]))
+    assert mp.paged_workspace_bytes(shape, 0) == 0
+    out, lse = torch.full((2, 4, D), 7.0, device="cuda"), torch.full((2, 4), 7.0, device="cuda")
+    mp.paged_attend(shape, q.cuda(), k.cuda(), v.cuda(), i32(table), i32([0, 0]), 0, out, lse,
+                    torch.empty(0, dtype=torch.uint8, device="cuda"))
+    assert (out == 0).all() and (lse == float("-inf")).all()
 
 
 def test_paged_moving_maximum():
@@ -490,6 +532,32 @@ def test_append_for_several_layers():
     c.check()
     c.k, c.v, c.rows = k2, v2, [(b, a) for a, b in c.rows]
     c.check()
+
+
+def test_pages_past_32_bits():
+    """Pools of more than 2^31 elements: append, decode, fork and copy on their last pages."""
+    hkv, size, P = 8, 16, 131100
+    assert (P - 9) * hkv * size * D > 1 << 31
+    shape = mp.PagesShape(3, 16, hkv, D, P, size, 4)
+    kp, vp = (torch.empty(P, hkv, size, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    refs = torch.ones(P, dtype=torch.int32, device="cuda")
+    refs[-9:] = 0
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    lens = i32([0, 0, 0])
+    mp.pages_reserve(shape, i32([40, 9, 0]), table, lens, refs)
+    assert table.tolist()[0][:3] == [P - 9, P - 8, P - 7] and table.tolist()[1][0] == P - 6
+    k, v, q = rand(49, hkv, D, seed=130), rand(49, hkv, D, seed=131), rand(3, 16, D, seed=132)
+    mp.paged_append(shape, k.cuda(), v.cuda(), table, lens, kp, vp, cu_new=i32([0, 40, 49, 49]))
+    copies = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    mp.pages_fork(shape, i32([0]), i32([2]), table, lens, refs, copies)
+    mp.pages_copy(shape, copies, kp, vp)
+    assert lens.tolist() == [40, 9, 40] and table.tolist()[2] == [P - 9, P - 8, P - 5, -1]
+    out, lse = torch.empty(3, 16, D, device="cuda"), torch.empty(3, 16, device="cuda")
+    ws = torch.empty(mp.paged_workspace_bytes(shape, 64), dtype=torch.uint8, device="cuda")
+    mp.paged_attend(shape, q.cuda(), kp, vp, table, lens, 64, out, lse, ws)
+    at = table.cpu()
+    local = torch.where(at >= 0, at - (P - 9), at)  # the last 9 pages as a pool of their own
+    check_paged(q, kp[-9:].cpu(), vp[-9:].cpu(), local.tolist(), [40, 9, 40], out.cpu(), lse.cpu())
 
 
 # ------------------------------------------------------------- a run of all ----
