@@ -11,8 +11,8 @@
 // tiles whose rows are (token, head of the group), so the G heads share every
 // K and V tile (kTok = 128 / G tokens a tile).  Key tiles are 128 tokens,
 // walked from the last visible one down to the first; a query tile joins at
-// its own last one.  One block per SM takes items in turn, longest first,
-// every second round in reverse (so the blocks' sums of work come out alike):
+// its own last one.  One block per SM lives on by taking over the blocks of the
+// grid that have not started yet, an item each, longest first:
 //   warps 0-3, 4-7  softmax of query tile 0, 1: thread = row.  S from TMEM,
 //                   P = 2^(s - m) in bf16 back into the columns of S, sum; at
 //                   the end of an item O / sum to memory.
@@ -41,12 +41,14 @@ constexpr int kHalfBytes = 128 * 128;         // 128 rows x 64 elements
 constexpr int kTileBytes = 2 * kHalfBytes;    // 32 KB
 constexpr int kSlots = 4;                     // ring of K and V tiles
 constexpr int kStageBytes = 4096;             // a softmax warp's stage for results: 32 rows x 64 dims
-constexpr int kItems = 4;                     // items known ahead
+constexpr int kItems = 2;                     // items known: the running one and the next
 constexpr int kFixes = 4;                     // more than the V tiles that the ring can hold
 constexpr int kSmemBytes = 1024 + (2 + kSlots) * kTileBytes + 8 * kStageBytes;
 constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpFix = 10, kWarpItems = 11;
 constexpr int kThreads = 32 * 12;
 constexpr uint32_t kColS = 0, kColO = 256;    // + 128 t
+constexpr long long kGroupBytes = 32ll << 20;  // K and V of the items in hand: a quarter of L2 (16 prompts of 8192
+                                               // tokens: 6.9 ms, without groups 8.4)
 constexpr float kMargin = 24.f;               // log2 units that a score may exceed its row's reference by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -70,7 +72,8 @@ enum {
     B_FIX = B_O + 2,           // [kFixes] V tile landed that has rows behind the sequence's end, in turn
     B_ITEM = B_FIX + kFixes,   // [kItems] item known
     B_TAKEN = B_ITEM + kItems, // [kItems] item done with by all roles
-    B_END = B_TAKEN + kItems,  // teardown
+    B_NEXT = B_TAKEN + kItems, // the next block's number is here
+    B_END = B_NEXT + 1,        // teardown
     kBars = B_END + 1
 };
 constexpr int kRoles = 8 + 3;  // warps that read an item
@@ -120,6 +123,29 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, uin
             dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
+}
+
+// Takes the next block of the grid that has not started: it will not start
+// any more, and its number arrives at dst (16 bytes) and completes on bar.
+__device__ __forceinline__ void next_block(uint32_t dst, uint32_t bar)
+{
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+                 "r"(bar)
+                 : "memory");
+}
+// False: there was none left (and none may be asked for again).
+__device__ __forceinline__ bool block_taken(uint32_t src, int &block)
+{
+    uint32_t ok, x;
+    asm volatile(
+        "{\n .reg .b128 h;\n .reg .pred p;\n ld.shared.b128 h, [%2];\n"
+        " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+        " @p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n}\n"
+        : "=r"(ok), "=r"(x)
+        : "r"(src)
+        : "memory");
+    if (ok) block = (int)x;
+    return ok != 0;
 }
 
 // K-major operand, 128B swizzle: rows of 128 B, 8-row groups 1024 B apart.
@@ -377,43 +403,103 @@ __device__ __forceinline__ int seq_rows(const Args &a, int b, int &row0)
     return lo < 0 || hi < lo || hi > a.s.T ? 0 : hi - lo;
 }
 
-// Items by rank, longest rows first.  With c_b = ceil(n_b / M) items in
-// sequence b (M tokens each), F(x) = sum_b max(0, c_b - x) items have index >=
-// x in their sequence; rank r has the largest index x with F(x) > r, in the
-// (r - F(x + 1))-th sequence that has one.  Ranks are asked for in rising
-// order, so x only falls.  Run by one warp.
+// Items by rank.  Sequences whose K and V together fit kGroupBytes form a
+// group (a longer one goes alone, as many kv heads at a time as fit), and the
+// groups follow one another, so that what the blocks read at a time stays in
+// L2.  Within a group the longest rows come first: with c_b = ceil(n_b / M)
+// items in sequence b (M tokens each), F(x) = sum_b max(0, c_b - x) items have
+// index >= x in their sequence; rank r has the largest index x with F(x) > r,
+// in the (r - F(x + 1))-th sequence that has one.  Ranks are asked for in
+// rising order, so groups only follow and x only falls.  Run by one warp.
 template <int M>
 struct ItemList {
     const Args &a;
-    int lane, x, fx;  // F(x) = fx, and F(x + 1) = above
-    int above;
+    int lane;
+    int base;            // rank of the group's first item
+    int b0, b1, h0, h1;  // sequences and kv heads of the group
+    int heads;           // kv heads a group of this sequence takes
+    int x, fx, above;    // F(x) = fx, F(x + 1) = above
+    int last;            // rank asked for last
+    __device__ __forceinline__ ItemList(const Args &args, int ln) : a(args), lane(ln) { start(); }
+    __device__ __forceinline__ void start()
+    {
+        last = base = b0 = b1 = x = fx = above = 0;
+        h0 = h1 = heads = a.s.Hkv;
+    }
+    __device__ __forceinline__ int items(int b) const
+    {
+        int row0;
+        return (seq_rows(a, b, row0) + M - 1) / M;
+    }
     __device__ __forceinline__ int F(int y) const
     {
-        int f = 0, row0;
-        for (int b = lane; b < a.s.B; b += 32) f += max((seq_rows(a, b, row0) + M - 1) / M - y, 0);
+        int f = 0;
+        for (int b = b0 + lane; b < b1; b += 32) f += max(items(b) - y, 0);
         return __reduce_add_sync(0xffffffffu, f);
     }
-    __device__ __forceinline__ ItemList(const Args &args, int ln) : a(args), lane(ln)
+    __device__ __forceinline__ bool next_group()
     {
-        int most = 0, row0;
-        for (int b = lane; b < a.s.B; b += 32) most = max(most, (seq_rows(a, b, row0) + M - 1) / M);
+        base += fx * (h1 - h0);  // x = 0 here: fx is all of the last group
+        if (h1 < a.s.Hkv) {
+            h0 = h1;
+            h1 = min(h0 + heads, a.s.Hkv);
+        } else {
+            if (b1 >= a.s.B) return false;
+            b0 = b1;
+            const long long most = kGroupBytes / (2 * 2 * kHeadDim * (long long)a.s.Hkv);  // tokens
+            long long sum = 0;
+            if (a.s.T <= most) b1 = a.s.B;  // all of them
+            for (bool open = true; open && b1 < a.s.B;) {
+                int row0;
+                const int n = b1 + lane < a.s.B ? seq_rows(a, b1 + lane, row0) : 0;
+                long long pre = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+                    if (lane >= o) pre += y;
+                }
+                const unsigned over = __ballot_sync(0xffffffffu, sum + pre > most);
+                const int fit = over ? __ffs((int)over) - 1 : 32;
+                if (fit > 0) sum += __shfl_sync(0xffffffffu, pre, fit - 1);
+                b1 = min(b1 + fit, a.s.B);
+                open = fit == 32;
+            }
+            heads = a.s.Hkv;
+            if (b1 == b0) {  // one that does not fit
+                int row0;
+                const int n = seq_rows(a, b1++, row0);
+                heads = max((int)(kGroupBytes / (2 * 2 * kHeadDim) / n), 1);
+            }
+            h0 = 0;
+            h1 = min(heads, a.s.Hkv);
+        }
+        int most = 0;
+        for (int b = b0 + lane; b < b1; b += 32) most = max(most, items(b));
         x = __reduce_max_sync(0xffffffffu, most);
         fx = above = 0;
+        return true;
     }
     __device__ __forceinline__ bool get(int r, Item &it)
     {
-        it.kvh = r % a.s.Hkv;
-        r /= a.s.Hkv;
-        while (fx <= r) {
-            if (x == 0) return false;
-            x--;
-            above = fx;
-            fx = F(x);
+        if (r < last) start();  // (blocks are handed out in rising order)
+        last = r;
+        int k;
+        for (;;) {
+            const int nh = max(h1 - h0, 1);
+            k = (r - base) / nh;
+            it.kvh = h0 + (r - base) % nh;
+            while (fx <= k && x > 0) {
+                x--;
+                above = fx;
+                fx = F(x);
+            }
+            if (fx > k) break;
+            if (!next_group()) return false;
         }
-        int k = r - above;
-        for (int b0 = 0; b0 < a.s.B; b0 += 32) {
+        k -= above;
+        for (int b = b0; b < b1; b += 32) {
             int row0 = 0, n = 0;
-            if (b0 + lane < a.s.B) n = seq_rows(a, b0 + lane, row0);
+            if (b + lane < b1) n = seq_rows(a, b + lane, row0);
             const unsigned has = __ballot_sync(0xffffffffu, (n + M - 1) / M > x);
             const int here = __popc(has);
             if (k < here) {
@@ -474,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kBars];
     __shared__ uint32_t tmem_sh;
+    __shared__ __align__(16) uint4 next_sh;
     __shared__ Item items[kItems];
     __shared__ volatile int abort_flag;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -489,6 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bar(i), i >= B_P && i < B_P + 4 ? 4 : i >= B_TAKEN && i < B_TAKEN + kItems ? kRoles : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == kWarpLoad && lane < 3)  // the descriptors are ready when the first item is
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(lane == 0 ? &mq : lane == 1 ? &mk : &mv)) : "memory");
     // rows of a query tile that no (token, head) fills: the copies never write them
     if (kTok * G < kRows && warp < 8) {
         for (int i = tid; i < 2 * 2 * (kRows - kTok * G) * 8; i += 256) {
@@ -519,16 +608,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lo < 0 || hi < lo || hi > a.s.T) set_status(a.status, MP_ERR_CAPACITY);
             }
         ItemList<2 * kTok> list(a, lane);
-        const int C = gridDim.x, c = blockIdx.x;
-        for (int k = 0;; k++) {
-            const bool live = list.get(k * C + ((k & 1) ? C - 1 - c : c), it);
-            if (k >= kItems && !wwait(B_TAKEN + k % kItems, (k / kItems - 1) & 1)) break;
+        int r = blockIdx.x;  // its own item, then those of blocks that have not started yet
+        bool more = true, live = true;
+        for (int k = 0; more; k++) {
+            if (live && k >= kItems && !wwait(B_TAKEN + k % kItems, (k / kItems - 1) & 1)) break;
+            if (k > 0) {
+                if (lane == 0) {
+                    fence_proxy_async_smem();
+                    mbar_expect_tx(bar(B_NEXT), 16);
+                    next_block(smem_u32(&next_sh), bar(B_NEXT));
+                }
+                __syncwarp();
+                if (!wwait(B_NEXT, (k - 1) & 1)) break;
+                more = block_taken(smem_u32(&next_sh), r);
+                __syncwarp();
+            }
+            if (!live) continue;  // past the last item: the blocks that are left have none either
+            live = more && list.get(r, it);
             if (!live) it.n = 0;
             if (lane == 0) {
                 items[k % kItems] = it;
                 mbar_arrive(bar(B_ITEM + k % kItems));
             }
-            if (!live) break;
         }
     } else if (warp == kWarpLoad) {
         // -------------------------------------------------------- producer ----
@@ -808,13 +909,12 @@ static cudaError_t launch_g(const PromptShape &s, const uint16_t *q, const uint1
     if (!make_map(&mq, q, s.T, s.Hq, s.qs, G, kTok) || !make_map(&mk, k, s.T, s.Hkv, s.ks, 1, kKeys) ||
         !make_map(&mv, v, s.T, s.Hkv, s.vs, 1, kKeys))
         return cudaErrorInvalidValue;
-    const long long items = ((long long)s.T / (2 * kTok) + s.B) * s.Hkv;  // sum ceil(n_b / M) <= T / M + B
+    const long long items = ((long long)s.T / (2 * kTok) + (s.B < s.T ? s.B : s.T)) * s.Hkv;  // sum ceil(n_b / M), at most
     if (items > 0x7fffffffll) return cudaErrorInvalidValue;
     const void *fn = reinterpret_cast<const void *>(prompt_attend_kernel<G>);
     cudaError_t e = ensure_smem(fn, kSmemBytes);
     if (e != cudaSuccess) return e;
-    static const int kSms = 148;
-    return launch_pdl(prompt_attend_kernel<G>, dim3((unsigned)(items < kSms ? items : kSms)), dim3(kThreads), kSmemBytes, st, mq, mk, mv, a);
+    return launch_pdl(prompt_attend_kernel<G>, dim3((unsigned)items), dim3(kThreads), kSmemBytes, st, mq, mk, mv, a);
 }
 
 }  // namespace prompt
