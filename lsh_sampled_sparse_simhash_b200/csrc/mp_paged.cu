@@ -37,7 +37,7 @@ constexpr int kStages = 3;
 constexpr int kRowBytes = 256;
 constexpr int kTileBytes = 2 * kTile * kRowBytes;        // K rows, then V rows
 constexpr int kRingBytes = kWarps * kStages * kTileBytes; // 96 KB
-constexpr int kAccBytes = kWarps * 8 * kHeadDim * 4;      // the warps' sums, where they are joined
+constexpr int kAccBytes = 2 * kWarps * 4 * kHeadDim * 4;  // the warps' sums of four heads, where they are joined: two in turn
 constexpr int kSmemBytes = kRingBytes + kAccBytes;        // 112 KB: two thread blocks per SM
 constexpr int kBlocksPerSm = 2;
 constexpr int kMergeWarps = 4, kMergeBatch = 4;
@@ -50,6 +50,7 @@ struct Args {
     const uint16_t *q, *kp, *vp;
     const int32_t *table, *lens;
     int max_len, C;
+    uint32_t magic;  // floor(2^32 / page_size) + 1, for tokens / page_size
     float *out, *lse;
     float *pml;   // [C][2][8][2]: m, l (log2 units) of the partials
     float *pacc;  // [C][2][8][128]
@@ -99,6 +100,19 @@ __device__ __forceinline__ int clamped_len(const Args &a, int b)
     return min(max(a.lens[b], 0), a.max_len);
 }
 __device__ __forceinline__ int blocks_of(int len) { return (len + kBlockTok - 1) / kBlockTok; }
+
+// tok / page_size and the remainder: the product's high word is the quotient
+// or one more (tokens are below 2^30).
+__device__ __forceinline__ int page_of(const Args &a, int tok, int &off)
+{
+    int q = a.s.S == 1 ? tok : (int)__umulhi((uint32_t)tok, a.magic);
+    off = tok - q * a.s.S;
+    if (off < 0) {
+        q--;
+        off += a.s.S;
+    }
+    return q;
+}
 
 // Sum over the sequences of their 64-token blocks; with `upto` given, only
 // those before it.
@@ -154,7 +168,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ uint32_t seen_sh[kWarps][kStages];  // bit i: token i of the stage's tile counts
-    __shared__ float red_ml[kWarps][2][8];
+    __shared__ float red_sh[2][kWarps][2][8];
     const PagesShape &s = a.s;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g4 = lane >> 2, t4 = lane & 3;  // mma fragment row and column group
@@ -201,17 +215,21 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     Walk at = rd;  // what is computed next, kStages - 1 blocks behind
 
     const uint32_t my_ring = smem_u32(ring) + (uint32_t)(warp * kStages * kTileBytes);
-    float *acc_sh = reinterpret_cast<float *>(ring + kRingBytes);  // [warp][8 heads][128], columns swizzled by head
-    auto acc_at = [&](int w, int h, int d) -> float & { return acc_sh[(w * 8 + h) * kHeadDim + (d ^ ((h >> 1) << 3))]; };
+    float *acc_sh = reinterpret_cast<float *>(ring + kRingBytes);  // [2][warp][4 heads][128], columns swizzled by head
+    int turn = 0, red = 0;  // which of the two joins are in
+    auto acc_at = [&](int w, int h, int d) -> float & {
+        return acc_sh[((turn * kWarps + w) * 4 + (h & 3)) * kHeadDim + (d ^ ((h & 2) << 2))];
+    };
 
     // The table entry of the next tile is fetched a tile ahead of its copies:
     // lane i < 16 holds that of token i (ALIGNED: all lanes the tile's one).
-    int tok0 = 0, page = -1;
+    int tok0 = 0, page = -1, off_pg = 0;  // off_pg: the token's row in its page
     auto fetch = [&]() {
         if (rd.left <= 0) return;
         tok0 = (rd.blk * kWarps + warp) * kTile;
         const int tok = ALIGNED ? tok0 : tok0 + (lane & 15);
-        page = tok < rd.len ? a.table[(size_t)rd.b * s.M + tok / s.S] : -2;
+        const int col = page_of(a, tok, off_pg);
+        page = tok < rd.len ? a.table[(size_t)rd.b * s.M + col] : -2;
         if (rd.blk == 0 && lane < 2 * s.G)  // a unit begins: its queries (2 lines a head) into L1
             asm volatile("prefetch.global.L1 [%0];" ::"l"(
                 a.q + ((size_t)rd.b * s.Hq + rd.kvh * s.G) * kHeadDim + lane * 64));
@@ -227,7 +245,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             if (ALIGNED) {
                 const int n = good ? min(rd.len - tok0, kTile) : 0;  // rows that count
                 seen = (1u << max(n, 0)) - 1u;
-                const size_t off = (((size_t)max(page, 0) * s.Hkv + rd.kvh) * s.S + tok0 % s.S + r0) * kHeadDim + p * 8;
+                const size_t off = (((size_t)max(page, 0) * s.Hkv + rd.kvh) * s.S + off_pg + r0) * kHeadDim + p * 8;
                 const uint16_t *k0 = a.kp + (good ? off : 0), *v0 = a.vp + (good ? off : 0);
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
@@ -238,7 +256,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
                 }
             } else {
                 // lanes 0..15: the row of token tok0 + lane in the pools (-1: none)
-                const long long row = good ? ((long long)page * s.Hkv + rd.kvh) * s.S + (tok0 + p) % s.S : -1;
+                const long long row = good ? ((long long)page * s.Hkv + rd.kvh) * s.S + off_pg : -1;
                 seen = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
@@ -287,13 +305,15 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             const unsigned seen = seen_sh[warp][slot];
             slot = slot == kStages - 1 ? 0 : slot + 1;
             // S^T: 16 tokens x 8 heads
-            float c0 = 0.f, c1 = 0.f, c2 = 0.f, c3 = 0.f;
+            float sc[2][4] = {};  // two chains of products
 #pragma unroll
             for (int ks = 0; ks < 8; ks++) {
                 uint32_t r0, r1, r2, r3;
                 ldmatrix_x4_s(r0, r1, r2, r3, kt + row_off(lane & 15, 2 * ks + (lane >> 4)));
-                mma_bf16_16816(c0, c1, c2, c3, r0, r1, r2, r3, qf[ks][0], qf[ks][1]);
+                float(&d)[4] = sc[ks & 1];
+                mma_bf16_16816(d[0], d[1], d[2], d[3], r0, r1, r2, r3, qf[ks][0], qf[ks][1]);
             }
+            float c0 = sc[0][0] + sc[1][0], c1 = sc[0][1] + sc[1][1], c2 = sc[0][2] + sc[1][2], c3 = sc[0][3] + sc[1][3];
             const bool s0 = (seen >> g4) & 1u, s1 = (seen >> (g4 + 8)) & 1u;
             c0 = s0 ? c0 * scale2 : -INFINITY;
             c1 = s0 ? c1 * scale2 : -INFINITY;
@@ -362,46 +382,59 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             l0 += __shfl_xor_sync(0xffffffffu, l0, w);
             l1 += __shfl_xor_sync(0xffffffffu, l1, w);
         }
+        // (two buffers in turn: whoever writes one again has met, in the join between, all that read it)
+        float(&red_ml)[kWarps][2][8] = red_sh[red];
+        red ^= 1;
         if (g4 == 0) {
             red_ml[warp][0][h0] = m0;
             red_ml[warp][0][h1] = m1;
             red_ml[warp][1][h0] = l0;
             red_ml[warp][1][h1] = l1;
         }
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            acc_at(warp, h0, i * 16 + g4) = o[i][0];
-            acc_at(warp, h1, i * 16 + g4) = o[i][1];
-            acc_at(warp, h0, i * 16 + g4 + 8) = o[i][2];
-            acc_at(warp, h1, i * 16 + g4 + 8) = o[i][3];
-        }
-        __syncthreads();
         const bool whole = blk0 == 0 && nt == nb;
         const int part = c * 2 + (blk0 == 0 ? 1 : 0);
-        for (int h = 0; h < s.G; h++) {  // thread = dim
-            float m = -INFINITY;
+        for (int q = 0; q < s.G; q += 4) {  // four heads at a time
+            if (h0 >> 2 == q >> 2) {
 #pragma unroll
-            for (int w = 0; w < kWarps; w++) m = fmaxf(m, red_ml[w][0][h]);
-            float l = 0.f, v = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; w++) {
-                const float f = red_ml[w][0][h] == -INFINITY ? 0.f : ex2(red_ml[w][0][h] - m);
-                l += f * red_ml[w][1][h];
-                v += f > 0.f ? f * acc_at(w, h, tid) : 0.f;
-            }
-            if (whole) {
-                const size_t bh = (size_t)b * s.Hq + hq0 + h;
-                a.out[bh * kHeadDim + tid] = l == 0.f ? 0.f : v / l;
-                if (tid == 0) a.lse[bh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-            } else {
-                a.pacc[((size_t)part * 8 + h) * kHeadDim + tid] = v;
-                if (tid == 0) {
-                    a.pml[((size_t)part * 8 + h) * 2] = m;
-                    a.pml[((size_t)part * 8 + h) * 2 + 1] = l;
+                for (int i = 0; i < 8; i++) {
+                    acc_at(warp, h0, i * 16 + g4) = o[i][0];
+                    acc_at(warp, h1, i * 16 + g4) = o[i][1];
+                    acc_at(warp, h0, i * 16 + g4 + 8) = o[i][2];
+                    acc_at(warp, h1, i * 16 + g4 + 8) = o[i][3];
                 }
             }
+            __syncthreads();
+            const int h = q + warp;  // a warp a head, a lane four dims
+            if (h < s.G) {
+                float mw[kWarps], l = 0.f;
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) mw[w] = red_ml[w][0][h];
+                const float m = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
+#pragma unroll
+                for (int w = 0; w < kWarps; w++) {
+                    if (mw[w] == -INFINITY) continue;
+                    const float f = ex2(mw[w] - m);
+                    const float4 x = *reinterpret_cast<const float4 *>(&acc_at(w, h, 4 * lane));
+                    l = fmaf(f, red_ml[w][1][h], l);
+                    v.x = fmaf(f, x.x, v.x);
+                    v.y = fmaf(f, x.y, v.y);
+                    v.z = fmaf(f, x.z, v.z);
+                    v.w = fmaf(f, x.w, v.w);
+                }
+                if (whole) {
+                    const size_t bh = (size_t)b * s.Hq + hq0 + h;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    reinterpret_cast<float4 *>(a.out + bh * kHeadDim)[lane] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+                    if (lane == 0) a.lse[bh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                } else {
+                    const size_t e = (size_t)part * 8 + h;
+                    reinterpret_cast<float4 *>(a.pacc + e * kHeadDim)[lane] = v;
+                    if (lane == 0) reinterpret_cast<float2 *>(a.pml)[e] = make_float2(m, l);
+                }
+            }
+            turn ^= 1;
         }
-        __syncthreads();  // acc_sh and red_ml are free again
     }
     cp_async_wait<0>();
 }
@@ -491,6 +524,7 @@ cudaError_t launch_paged_attend(const PagesShape &s, const uint16_t *q, const ui
     a.table = table;
     a.lens = lens;
     a.max_len = max_len;
+    a.magic = (uint32_t)((1ull << 32) / (uint64_t)s.S) + 1u;
     a.C = paged::num_runs(s, max_len);
     a.out = out;
     a.lse = lse;
