@@ -161,6 +161,34 @@ struct Walk {
     }
 };
 
+// Where block x of the line lies (32 sequences a step).
+__device__ __forceinline__ void locate(const Args &a, long long x, int lane, Walk &w)
+{
+    long long first = 0;  // the line's position of the step's first sequence
+    for (int b0 = 0;; b0 += 32) {
+        const int bb = b0 + lane;
+        const long long n = bb < a.s.B ? (long long)blocks_of(clamped_len(a, bb)) * a.s.Hkv : 0;
+        long long pre = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, pre, o);
+            if (lane >= o) pre += y;
+        }
+        const unsigned over = __ballot_sync(0xffffffffu, first + pre > x);
+        if (over) {
+            const int l = __ffs((int)over) - 1;
+            w.b = b0 + l;
+            first += __shfl_sync(0xffffffffu, pre - n, l);
+            break;
+        }
+        first += __shfl_sync(0xffffffffu, pre, 31);
+    }
+    w.len = clamped_len(a, w.b);
+    w.nb = blocks_of(w.len);
+    w.kvh = (int)((x - first) / w.nb);
+    w.blk = (int)((x - first) % w.nb);
+}
+
 // ALIGNED: pages are whole tiles (page_size % 16 == 0), so a tile lies in one
 // page and its table entry is read once, not per row.
 template <bool ALIGNED>
@@ -182,36 +210,16 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     if (c == 0)
         for (int j = tid; j < s.B; j += blockDim.x)
             if (a.lens[j] > a.max_len || a.lens[j] < 0) set_status(a.status, MP_ERR_CAPACITY);
+    for (int j = c; j < s.B; j += gridDim.x)  // sequences without tokens
+        if (clamped_len(a, j) == 0) {
+            for (int i = tid; i < s.Hq * kHeadDim; i += blockDim.x) a.out[(size_t)j * s.Hq * kHeadDim + i] = 0.f;
+            for (int i = tid; i < s.Hq; i += blockDim.x) a.lse[(size_t)j * s.Hq + i] = -INFINITY;
+        }
     if (c >= C) return;
     const long long x = c * W / C;
-    // the sequence that x falls into: 32 sequences a step
     Walk rd;  // what is read next
     rd.left = (c + 1) * W / C - x;
-    {
-        long long first = 0;  // the line's position of the step's first sequence
-        for (int b0 = 0;; b0 += 32) {
-            const int bb = b0 + lane;
-            const long long n = bb < s.B ? (long long)blocks_of(clamped_len(a, bb)) * s.Hkv : 0;
-            long long pre = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, pre, o);
-                if (lane >= o) pre += y;
-            }
-            const unsigned over = __ballot_sync(0xffffffffu, first + pre > x);
-            if (over) {
-                const int l = __ffs((int)over) - 1;
-                rd.b = b0 + l;
-                first += __shfl_sync(0xffffffffu, pre - n, l);
-                break;
-            }
-            first += __shfl_sync(0xffffffffu, pre, 31);
-        }
-        rd.len = clamped_len(a, rd.b);
-        rd.nb = blocks_of(rd.len);
-        rd.kvh = (int)((x - first) / rd.nb);
-        rd.blk = (int)((x - first) % rd.nb);
-    }
+    locate(a, x, lane, rd);
     Walk at = rd;  // what is computed next, kStages - 1 blocks behind
 
     const uint32_t my_ring = smem_u32(ring) + (uint32_t)(warp * kStages * kTileBytes);
@@ -439,32 +447,33 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     cp_async_wait<0>();
 }
 
-// Joins the partials of the units that several runs share, and writes the
-// units without tokens.  A block per (sequence, query head): its warps take
-// the runs in turn (lane = 4 dims), kMergeBatch loads in flight each, then
+// Joins the partials of the units that several runs share.  Block (c, head of
+// the group): the unit that run c ends, if it began in a run before.  Its warps
+// take the runs in turn (lane = 4 dims), kMergeBatch loads in flight each, then
 // meet in shared memory.
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_partials_kernel(const Args a)
 {
     __shared__ float red_m[kMergeWarps], red_l[kMergeWarps];
     __shared__ float4 red_v[kMergeWarps][32];
     const PagesShape &s = a.s;
-    const int bh = blockIdx.x, b = bh / s.Hq, hq = bh % s.Hq, kvh = hq / s.G, h = hq % s.G;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int c1 = blockIdx.x + 1, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the lengths are older than this kernel's predecessor: read before the wait
-    const int nb = blocks_of(clamped_len(a, b));
-    const long long before = blocks_before(a, b, lane), W = blocks_before(a, s.B, lane) * s.Hkv;
-    const long long x0 = before * s.Hkv + (long long)kvh * nb;
-    int c0 = 0, c1 = 0;
-    if (nb > 0) {
-        const int C = live_runs(W, a.C);
-        c0 = run_of(x0, W, C);
-        c1 = run_of(x0 + nb - 1, W, C);
+    const long long W = blocks_before(a, s.B, lane) * s.Hkv;
+    const int C = live_runs(W, a.C);
+    int c0 = 0;
+    Walk u;
+    bool mine = false;
+    if (c1 < C) {
+        const long long x = c1 * W / C;
+        locate(a, x, lane, u);
+        mine = u.blk > 0 && x - u.blk + u.nb <= (c1 + 1) * W / C;
+        c0 = run_of(x - u.blk, W, C);
     }
     grid_dependency_wait();
-    if (nb > 0 && c0 == c1) return;  // one run held it all and wrote the result
+    if (!mine) return;
     float m = -INFINITY, l = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int cb = c0 + warp; nb > 0 && cb <= c1; cb += kMergeWarps * kMergeBatch) {
+    for (int cb = c0 + warp; cb <= c1; cb += kMergeWarps * kMergeBatch) {
         float2 ml[kMergeBatch];
         float4 acc[kMergeBatch];
 #pragma unroll
@@ -491,8 +500,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_partials_kernel(const 
 #pragma unroll
     for (int w = 1; w < kMergeWarps; w++)
         if (red_m[w] != -INFINITY) fold(m, l, v, red_m[w], red_l[w], red_v[w][lane]);
+    const size_t bh = (size_t)u.b * s.Hq + u.kvh * s.G + h;
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    reinterpret_cast<float4 *>(a.out + (size_t)bh * kHeadDim)[lane] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    reinterpret_cast<float4 *>(a.out + bh * kHeadDim)[lane] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
     if (lane == 0) a.lse[bh] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
@@ -531,14 +541,12 @@ cudaError_t launch_paged_attend(const PagesShape &s, const uint16_t *q, const ui
     a.pacc = static_cast<float *>(workspace);
     a.pml = a.pacc + (size_t)a.C * 2 * 8 * kHeadDim;
     a.status = status;
-    if (a.C > 0) {
-        auto kernel = s.S % paged::kTile == 0 ? paged::paged_attend_kernel<true> : paged::paged_attend_kernel<false>;
-        cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), paged::kSmemBytes);
-        if (e != cudaSuccess) return e;
-        e = launch_pdl(kernel, dim3(a.C), dim3(32 * paged::kWarps), paged::kSmemBytes, st, a);
-        if (e != cudaSuccess) return e;
-    }
-    return launch_pdl(paged::merge_partials_kernel, dim3(s.B * s.Hq), dim3(32 * paged::kMergeWarps), 0, st, a);
+    auto kernel = s.S % paged::kTile == 0 ? paged::paged_attend_kernel<true> : paged::paged_attend_kernel<false>;
+    cudaError_t e = ensure_smem(reinterpret_cast<const void *>(kernel), paged::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kernel, dim3(a.C > 0 ? a.C : 1), dim3(32 * paged::kWarps), paged::kSmemBytes, st, a);
+    if (e != cudaSuccess || a.C < 2) return e;  // one run: no unit is cut
+    return launch_pdl(paged::merge_partials_kernel, dim3(a.C - 1, s.G), dim3(32 * paged::kMergeWarps), 0, st, a);
 }
 
 }  // namespace mp
