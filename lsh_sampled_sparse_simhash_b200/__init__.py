@@ -5,6 +5,22 @@ the C ABI of ``include/magicpig.h``); this package is a thin ctypes binding
 that marshals torch tensors (device memory and streams only) into those calls.
 There is no fallback: if the library is missing or cannot load, every call
 raises.
+
+Beside the sampled decode: causal attention over packed prompts
+(``prompt_attend``), exact decode over a paged key-value cache
+(``paged_attend``), the append into its pages (``paged_append``) and the
+operations on them (``pages_reserve``, ``pages_fork``, ``pages_free``,
+``pages_compact``, ``pages_copy``).  A cache from prompt to prompt::
+
+    pages_reserve(shape, lens_of_new, table, lens, refs)       # pages for the prompts
+    prompt_attend(prompt_shape, q, k, v, cu, out, lse)          # every layer
+    paged_append(shape, k, v, table, lens, k_pages, v_pages, cu_new=cu)
+    pages_fork(shape, src, dst, table, lens, refs, copies)      # n answers to one prompt
+    pages_copy(shape, copies, k_pages, v_pages)                 # every layer
+    pages_reserve(shape, ones, table, lens, refs)               # each step: a page where one is needed,
+    paged_append(shape, k_new, v_new, table, lens, k_pages, v_pages)
+    paged_attend(shape, q, k_pages, v_pages, table, lens, max_len, out, lse, workspace)
+    pages_free(shape, ended, table, lens, refs)
 """
 from ._binding import (  # noqa: F401
     MagicPIGError,

@@ -4,7 +4,11 @@
 //   s_ih = q_h . k_i / sqrt(d),  out_h = sum_i e^{s_ih} v_i / sum_i e^{s_ih},
 // one pass over the unit's tokens with a running maximum and sum per head.
 // The floor is HBM: 512 bytes per (token, kv head), each read once; the
-// products are 2 d G multiply-adds on them, far below the tensor rate.
+// products are 2 d G multiply-adds on them, far below the tensor rate.  Measured
+// with 32 / 8 heads, 16 sequences of 32k to 131k tokens in pages of 16: 784 us
+// for 5.46 GB, 7.0 TB/s (a copy runs at 6.55); one sequence of 16k 19 us (floor
+// 10: launches, the first loads' latency and the join are the rest); 256 of up
+// to 300 50 us (floor 25: the joins at the units' ends).
 //
 // Split: the 64-token blocks of all units, unit after unit, form one line of
 // W blocks, and the C thread blocks of the grid (two per SM) take equal runs

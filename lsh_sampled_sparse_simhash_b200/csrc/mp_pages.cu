@@ -9,10 +9,13 @@
 // run knows every page's rank.  Whole numbers only, no order that depends on
 // timing: the same call always takes the same pages.
 //
-// These calls move a few hundred kilobytes at most and are bound by latency
-// (dependent loads and cluster barriers).  A cluster, and not more blocks,
-// because its barrier costs under a microsecond while a second launch costs
-// two.  Loads of the counts bypass L1 (ld.global.cg): other blocks of the
+// The plans move a few hundred kilobytes at most and are bound by latency
+// (dependent loads and cluster barriers): ending 40 of 256 sequences and
+// reserving for the rest takes 15 us with 124k pages and 1000 columns, a
+// compaction plan of 2900 pages 9 us.  A cluster, and not more blocks, because
+// its barrier costs under a microsecond while a second launch costs two.  The
+// page copies and the append are bound by HBM: 88 MB in 13 us (6.7 TB/s), 196
+// MB of a strided projection's rows in 28.5 us (6.9 TB/s).  Loads of the counts bypass L1 (ld.global.cg): other blocks of the
 // cluster change them between two barriers.
 #include <cooperative_groups.h>
 

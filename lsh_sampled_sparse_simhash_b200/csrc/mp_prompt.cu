@@ -4,8 +4,12 @@
 // For the token i of a sequence and a query head h of kv head u:
 //   s_j = q_ih . k_ju / sqrt(d),  out_ih = sum_{j <= i} e^{s_j} v_ju / sum_{j <= i} e^{s_j}
 // in one pass over the keys, with a running maximum and sum per row.  Bound by
-// the tensor rate (4 d multiply-adds a visible pair, 128^3 per tile product)
-// and, as closely, by the exponentials (one per pair).
+// the tensor rate (2 x 128^3 multiply-adds a tile of 128 rows and 128 keys) and,
+// as closely, by the exponentials (128^2 a tile, 16 a cycle and SM): 1024
+// cycles each at the nominal rates.  Measured at 16384 tokens, 32 / 8 heads:
+// 1.87 ms, 1180 TFLOP/s of causal work (72% of the measured burst rate of a
+// library product, 89% of its rate under the power cap, which holds here too),
+// tensor pipe and special functions 64% busy each.
 //
 // An item is 2 kTok tokens of one sequence and one kv head: two 128-row query
 // tiles whose rows are (token, head of the group), so the G heads share every
@@ -24,6 +28,18 @@
 //   warp 10         zeroes the rows of the last V tile behind the sequence's end.
 //   warp 11         finds the next items; holds the TMEM allocation.
 // TMEM: S0, S1, O0, O1, 128 columns each.
+//
+// Where a round (both query tiles over one key tile, about 3100 cycles) goes:
+// a tile's softmax takes 1950 and its products 1100 before the next S is there,
+// one after the other, and TMEM has no room for a third S.  The 32 products of
+// a round alone take 2580 (80 cycles each where 64 are nominal, alike with Q
+// from TMEM and without copies: an N = 128 product's own overhead), so no order
+// of the rest gets below that.  Measured and not kept: 16 softmax warps with 64
+// keys each (16k tokens 2.06 ms: they have to agree on the reference through
+// shared memory, whose bandwidth the products use up), key tiles of 64 with two
+// S each (products 3310 a round), an eighth to a half of the exponentials by a
+// polynomial (within 2%: the power cap), all 128 scores of a row in registers
+// (within 1%).
 //
 // Every wait is bounded (1 s); on expiry MP_ERR_CUDA is recorded and the block
 // winds down, waiting for its copies and products in flight.
