@@ -342,7 +342,8 @@ typedef struct mp_prompt_shape {
  *   cu_lens  int32 [B + 1] device, 4-byte aligned, not decreasing, from >= 0
  *      to <= T.  A sequence whose two entries break that is skipped and
  *      MP_ERR_CAPACITY recorded.
- *   out  bf16 [T][Hq][d]     lse  fp32 [T][Hq] (nullable)
+ *   out  bf16 [T][Hq][d]     lse  fp32 [T][Hq] (nullable); neither may overlap
+ *        q, k or v
  * Rows of no sequence (behind the last one, say) are neither used nor
  * written; what they hold in q, k and v, NaN included, has no effect.  Within
  * a sequence the values v must be finite: a value that is not reaches the

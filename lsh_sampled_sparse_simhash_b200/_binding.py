@@ -325,9 +325,9 @@ def _rows_arg(t, what: str, dtype, shape, device: int):
         _refuse(t, what, dtype, shape, device)
     rows, heads, d = shape
     s0, s1, s2 = t.stride()
-    if rows and (s2 != 1 or (heads > 1 and s1 != d)):
+    if rows and (s2 != 1 or (heads > 1 and s1 != d)) or rows > 1 and s0 < heads * d:
         _refuse(t, what, dtype, shape, device)
-    return t.data_ptr(), s0 if rows > 1 else 0
+    return t.data_ptr(), s0 if rows > 1 else 0  # (0 is "side by side" to the library)
 
 
 def _opt(t, what: str, dtype, shape, device: int) -> Optional[int]:

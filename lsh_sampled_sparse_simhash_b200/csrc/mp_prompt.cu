@@ -64,7 +64,7 @@ constexpr int kWarpMma = 8, kWarpLoad = 9, kWarpFix = 10, kWarpItems = 11;
 constexpr int kThreads = 32 * 12;
 constexpr uint32_t kColS = 0, kColO = 256;    // + 128 t
 constexpr long long kGroupBytes = 32ll << 20;  // K and V of the items in hand: a quarter of L2 (16 prompts of 8192
-                                               // tokens: 6.9 ms, without groups 8.4)
+                                               // tokens: 6.7 ms, without groups 8.4)
 constexpr float kMargin = 24.f;               // log2 units that a score may exceed its row's reference by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -84,7 +84,7 @@ enum {
     B_FREE = B_KV + kSlots,    // [kSlots] products on the slot complete
     B_S = B_FREE + kSlots,     // [2] S in TMEM (and all products before it complete)
     B_P = B_S + 2,             // [2][2] P of keys 0-63, 64-127 in TMEM, O rescaled (4 warps each)
-    B_O = B_P + 4,           // [2] the item's last product into O complete
+    B_O = B_P + 4,             // [2] the item's last product into O complete
     B_FIX = B_O + 2,           // [kFixes] V tile landed that has rows behind the sequence's end, in turn
     B_ITEM = B_FIX + kFixes,   // [kItems] item known
     B_TAKEN = B_ITEM + kItems, // [kItems] item done with by all roles

@@ -185,7 +185,7 @@ def test_binding_refuses_wrong_tensors():
     shape = mp.PromptShape(1, 4, 2, D, 20)
     for bad in ((dq.float(), dk, dv, dcu, out), (dq[:, :2], dk, dv, dcu, out), (dq, dk.transpose(0, 1), dv, dcu, out),
                 (dq, dk, dv[:10], dcu, out), (dq, dk, dv, dcu.long(), out), (dq, dk, dv, dcu, out.float()),
-                (dq, dk, v, dcu, out)):
+                (dq, dk, v, dcu, out), (dq[:1].expand(20, 4, D), dk, dv, dcu, out)):
         with pytest.raises(ValueError):
             mp.prompt_attend(shape, *bad)
     with pytest.raises(mp.MagicPIGError) as e:
