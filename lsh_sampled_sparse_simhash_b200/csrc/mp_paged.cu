@@ -5,16 +5,17 @@
 // one pass over the unit's tokens with a running maximum and sum per head.
 // The floor is HBM: 512 bytes per (token, kv head), each read once; the
 // products are 2 d G multiply-adds on them, far below the tensor rate.  Measured
-// with 32 / 8 heads, 16 sequences of 32k to 131k tokens in pages of 16: 784 us
+// with 32 / 8 heads, 16 sequences of 32k to 131k tokens in pages of 16: 776 us
 // for 5.46 GB, 7.0 TB/s (a copy runs at 6.55); one sequence of 16k 19 us (floor
 // 10: launches, the first loads' latency and the join are the rest); 256 of up
-// to 300 50 us (floor 25: the joins at the units' ends).
+// to 300 37 us (floor 25), 47 with units' ends counted as nothing.
 //
 // Split: the 64-token blocks of all units, unit after unit, form one line of
-// W blocks, and the C thread blocks of the grid (two per SM) take equal runs
-// of it, c W / C to (c + 1) W / C.  So every thread block reads the same
-// number of bytes whatever the lengths are, one long sequence is split over
-// all SMs and a batch of short ones hardly at all.  A run that covers a whole
+// W places (a unit's end takes kEndCost, as it costs about as much), and the C
+// thread blocks of the grid (two per SM) take equal runs of it, c W / C to
+// (c + 1) W / C.  So every thread block has the same work whatever the lengths
+// are, one long sequence is split over all SMs and a batch of short ones hardly
+// at all.  A run that covers a whole
 // unit writes its result; a unit cut by the ends of runs leaves one partial
 // (m, l, acc) per run, at most two per thread block, and merge_partials_kernel
 // joins them.
@@ -43,6 +44,7 @@ constexpr int kTileBytes = 2 * kTile * kRowBytes;        // K rows, then V rows
 constexpr int kRingBytes = kWarps * kStages * kTileBytes; // 96 KB
 constexpr int kAccBytes = 2 * kWarps * 4 * kHeadDim * 4;  // the warps' sums of four heads, where they are joined: two in turn
 constexpr int kSmemBytes = kRingBytes + kAccBytes;        // 112 KB: two thread blocks per SM
+constexpr int kEndCost = 1;                  // what a unit's end (its queries, the join) costs, in blocks
 constexpr int kBlocksPerSm = 2;
 constexpr int kMergeWarps = 4, kMergeBatch = 4;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -104,6 +106,8 @@ __device__ __forceinline__ int clamped_len(const Args &a, int b)
     return min(max(a.lens[b], 0), a.max_len);
 }
 __device__ __forceinline__ int blocks_of(int len) { return (len + kBlockTok - 1) / kBlockTok; }
+// Places of a unit on the line: its blocks, then its end.
+__device__ __forceinline__ int places_of(int nb) { return nb > 0 ? nb + kEndCost : 0; }
 
 // tok / page_size and the remainder: the product's high word is the quotient
 // or one more (tokens are below 2^30).
@@ -118,19 +122,45 @@ __device__ __forceinline__ int page_of(const Args &a, int tok, int &off)
     return q;
 }
 
-// Sum over the sequences of their 64-token blocks; with `upto` given, only
-// those before it.
-__device__ __forceinline__ long long blocks_before(const Args &a, int upto, int lane)
+// Inclusive prefix sums over a warp.
+__device__ __forceinline__ long long warp_prefix(long long v, int lane)
 {
-    long long n = 0;
-    for (int b = lane; b < upto; b += 32) n += blocks_of(clamped_len(a, b));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += y;
+    }
+    return v;
 }
 
+// The line as a warp sees it: lane l has the blocks of sequences l chunk to
+// (l + 1) chunk, and of all before.
+struct Line {
+    int chunk;
+    long long own, upto, W;
+    __device__ __forceinline__ Line(const Args &a, int lane)
+    {
+        constexpr int kLens = 2;
+        chunk = (a.s.B + 31) / 32;
+        long long n = 0;
+        for (int i0 = 0; i0 < chunk; i0 += kLens) {
+            int v[kLens];  // loads in flight
+#pragma unroll
+            for (int i = 0; i < kLens; i++) {
+                const int b = lane * chunk + i0 + i;
+                v[i] = i0 + i < chunk && b < a.s.B ? clamped_len(a, b) : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kLens; i++) n += places_of(blocks_of(v[i]));
+        }
+        own = n * a.s.Hkv;
+        upto = warp_prefix(own, lane);
+        W = __shfl_sync(0xffffffffu, upto, 31);
+    }
+};
+
 // Runs that the line is cut into: C, or W where that is less (so no run is
-// empty).  The run that holds block x is the largest c with c W / C <= x.
+// empty).  The run that holds place x is the largest c with c W / C <= x.
 __device__ __forceinline__ int live_runs(long long W, int C) { return (int)min(W, (long long)C); }
 __device__ __forceinline__ int run_of(long long x, long long W, int C) { return (int)(((x + 1) * C - 1) / W); }
 
@@ -149,12 +179,18 @@ __device__ __forceinline__ void fold(float &m, float &l, float4 &v, float m2, fl
 // A walk over a run of the line, block by block: unit after unit, the kv heads
 // of a sequence side by side, sequences without tokens passed over.
 struct Walk {
-    long long left;  // blocks of the run from here on
+    long long left;  // places of the run from here on
     int b, kvh, blk, len, nb;
     __device__ __forceinline__ void next(const Args &a)
     {
         left--;
-        if (++blk < nb || left <= 0) return;
+        if (++blk >= nb) next_unit(a, kEndCost);
+    }
+    // Past the places that are left of the unit's end.
+    __device__ __forceinline__ void next_unit(const Args &a, int end)
+    {
+        left -= end;
+        if (left <= 0) return;
         blk = 0;
         if (++kvh < a.s.Hkv) return;
         kvh = 0;
@@ -165,32 +201,42 @@ struct Walk {
     }
 };
 
-// Where block x of the line lies (32 sequences a step).
-__device__ __forceinline__ void locate(const Args &a, long long x, int lane, Walk &w)
+// Where place x of the line lies.
+__device__ __forceinline__ void locate(const Args &a, const Line &line, long long x, int lane, Walk &w)
 {
-    long long first = 0;  // the line's position of the step's first sequence
-    for (int b0 = 0;; b0 += 32) {
+    const int l = __ffs((int)__ballot_sync(0xffffffffu, line.upto > x)) - 1;  // the lane whose sequences hold it
+    long long first = __shfl_sync(0xffffffffu, line.upto - line.own, l);     // the line's position of the step's first sequence
+    for (int b0 = l * line.chunk;; b0 += 32) {
         const int bb = b0 + lane;
-        const long long n = bb < a.s.B ? (long long)blocks_of(clamped_len(a, bb)) * a.s.Hkv : 0;
-        long long pre = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, pre, o);
-            if (lane >= o) pre += y;
-        }
+        const long long n = bb < a.s.B ? (long long)places_of(blocks_of(clamped_len(a, bb))) * a.s.Hkv : 0;
+        const long long pre = warp_prefix(n, lane);
         const unsigned over = __ballot_sync(0xffffffffu, first + pre > x);
         if (over) {
-            const int l = __ffs((int)over) - 1;
-            w.b = b0 + l;
-            first += __shfl_sync(0xffffffffu, pre - n, l);
+            const int k = __ffs((int)over) - 1;
+            w.b = b0 + k;
+            first += __shfl_sync(0xffffffffu, pre - n, k);
             break;
         }
         first += __shfl_sync(0xffffffffu, pre, 31);
     }
     w.len = clamped_len(a, w.b);
     w.nb = blocks_of(w.len);
-    w.kvh = (int)((x - first) / w.nb);
-    w.blk = (int)((x - first) % w.nb);
+    w.kvh = (int)((x - first) / places_of(w.nb));
+    w.blk = (int)((x - first) - (long long)w.kvh * places_of(w.nb));  // nb and more: in the unit's end
+}
+
+// The K and V pieces of rows I, I + 1, .. (of 8) of a lane: 512 bytes apart in
+// the pools, swizzled in the ring (offsets as immediates).
+template <int I>
+__device__ __forceinline__ void copy_rows(const uint32_t (&d)[4], const uint16_t *k, const uint16_t *v)
+{
+    if constexpr (I < 8) {
+        asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %2], 16;\n" ::"r"(d[I & 3]), "l"(k), "n"(512 * I) : "memory");
+        asm volatile("cp.async.cg.shared.global [%0 + %2], [%1 + %3], 16;\n" ::"r"(d[I & 3]), "l"(v),
+                     "n"(512 * I + kTile * kRowBytes), "n"(512 * I)
+                     : "memory");
+        copy_rows<I + 1>(d, k, v);
+    }
 }
 
 // ALIGNED: pages are whole tiles (page_size % 16 == 0), so a tile lies in one
@@ -209,7 +255,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     grid_dependency_wait();
 
     // this thread block's run of the line
-    const long long W = blocks_before(a, s.B, lane) * s.Hkv;
+    const Line line(a, lane);
+    const long long W = line.W;
     const int c = blockIdx.x, C = live_runs(W, a.C);
     if (c == 0)
         for (int j = tid; j < s.B; j += blockDim.x)
@@ -223,7 +270,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     const long long x = c * W / C;
     Walk rd;  // what is read next
     rd.left = (c + 1) * W / C - x;
-    locate(a, x, lane, rd);
+    locate(a, line, x, lane, rd);
+    if (rd.blk >= rd.nb) rd.next_unit(a, rd.nb + kEndCost - rd.blk);
     Walk at = rd;  // what is computed next, kStages - 1 blocks behind
 
     const uint32_t my_ring = smem_u32(ring) + (uint32_t)(warp * kStages * kTileBytes);
@@ -246,6 +294,10 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             asm volatile("prefetch.global.L1 [%0];" ::"l"(
                 a.q + ((size_t)rd.b * s.Hq + rd.kvh * s.G) * kHeadDim + lane * 64));
     };
+    // row 2 i + lane / 16 of a tile goes to its swizzled place: lane_dst[i % 4] + 512 i
+    uint32_t lane_dst[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) lane_dst[i] = my_ring + row_off(2 * i + (lane >> 4), lane & 15) - 512 * i;
     int slot_rd = 0;
     auto issue = [&]() {
         if (rd.left > 0) {
@@ -257,14 +309,21 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             if (ALIGNED) {
                 const int n = good ? min(rd.len - tok0, kTile) : 0;  // rows that count
                 seen = (1u << max(n, 0)) - 1u;
-                const size_t off = (((size_t)max(page, 0) * s.Hkv + rd.kvh) * s.S + off_pg + r0) * kHeadDim + p * 8;
-                const uint16_t *k0 = a.kp + (good ? off : 0), *v0 = a.vp + (good ? off : 0);
+                const size_t off = good ? (((size_t)page * s.Hkv + rd.kvh) * s.S + off_pg + r0) * kHeadDim + p * 8 : 0;
+                const uint16_t *k0 = a.kp + off, *v0 = a.vp + off;
+                uint32_t d[4];
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const int r = 2 * i + r0, bytes = r < n ? 16 : 0;  // a row that does not count is zeros: 0 times anything else may be NaN
-                    const size_t o = r < n ? (size_t)(2 * i) * kHeadDim : 0;
-                    cp_async_16_s(dst + row_off(r, p), k0 + o, bytes);
-                    cp_async_16_s(dst + kTile * kRowBytes + row_off(r, p), v0 + o, bytes);
+                for (int i = 0; i < 4; i++) d[i] = lane_dst[i] + slot_rd * kTileBytes;
+                if (n == kTile) {
+                    copy_rows<0>(d, k0, v0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const int r = 2 * i + r0, bytes = r < n ? 16 : 0;  // a row that does not count is zeros: 0 times anything else may be NaN
+                        const size_t o = r < n ? (size_t)(2 * i) * kHeadDim : 0;
+                        cp_async_16_s(d[i & 3] + 512 * i, k0 + o, bytes);
+                        cp_async_16_s(d[i & 3] + 512 * i + kTile * kRowBytes, v0 + o, bytes);
+                    }
                 }
             } else {
                 // lanes 0..15: the row of token tok0 + lane in the pools (-1: none)
@@ -290,18 +349,21 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     fetch();
     for (int t = 0; t < kStages - 1; t++) issue();
 
-    int slot = 0;
-    while (at.left > 0) {
-        const int hq0 = at.kvh * s.G, b = at.b, nb = at.nb, blk0 = at.blk;
-        // query fragments: B of m16n8k16 (k = dims, n = heads), zero for heads past G
-        uint32_t qf[8][2];
+    // query fragments of a unit: B of m16n8k16 (k = dims, n = heads), zero for heads past G
+    uint32_t qf[8][2];
+    auto load_q = [&]() {
+        const uint16_t *qr = a.q + ((size_t)at.b * s.Hq + at.kvh * s.G + g4) * kHeadDim + t4 * 2;
 #pragma unroll
         for (int ks = 0; ks < 8; ks++)
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const uint16_t *qr = a.q + ((size_t)b * s.Hq + hq0 + g4) * kHeadDim + ks * 16 + j * 8 + t4 * 2;
-                qf[ks][j] = g4 < s.G ? __ldg(reinterpret_cast<const uint32_t *>(qr)) : 0u;
-            }
+            for (int j = 0; j < 2; j++)
+                qf[ks][j] = g4 < s.G ? __ldg(reinterpret_cast<const uint32_t *>(qr + ks * 16 + j * 8)) : 0u;
+    };
+    load_q();
+
+    int slot = 0;
+    while (at.left > 0) {
+        const int hq0 = at.kvh * s.G, b = at.b, nb = at.nb, blk0 = at.blk;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
         float o[8][4];
 #pragma unroll
@@ -388,6 +450,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
             issue();
             at.next(a);
         }
+        if (at.left > 0) load_q();  // of the next unit, under the join
         // ---- the warps' states, joined in shared memory (copies of what follows are in flight) ----
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) {
@@ -407,12 +470,13 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
         const int part = c * 2 + (blk0 == 0 ? 1 : 0);
         for (int q = 0; q < s.G; q += 4) {  // four heads at a time
             if (h0 >> 2 == q >> 2) {
+                float *lo = &acc_at(warp, h0, g4), *hi = &acc_at(warp, h0, g4 + 8);  // h1: the next row, alike
 #pragma unroll
                 for (int i = 0; i < 8; i++) {
-                    acc_at(warp, h0, i * 16 + g4) = o[i][0];
-                    acc_at(warp, h1, i * 16 + g4) = o[i][1];
-                    acc_at(warp, h0, i * 16 + g4 + 8) = o[i][2];
-                    acc_at(warp, h1, i * 16 + g4 + 8) = o[i][3];
+                    lo[i * 16] = o[i][0];
+                    lo[i * 16 + kHeadDim] = o[i][1];
+                    hi[i * 16] = o[i][2];
+                    hi[i * 16 + kHeadDim] = o[i][3];
                 }
             }
             __syncthreads();
@@ -462,15 +526,16 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_partials_kernel(const 
     const PagesShape &s = a.s;
     const int c1 = blockIdx.x + 1, h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the lengths are older than this kernel's predecessor: read before the wait
-    const long long W = blocks_before(a, s.B, lane) * s.Hkv;
+    const Line line(a, lane);
+    const long long W = line.W;
     const int C = live_runs(W, a.C);
     int c0 = 0;
     Walk u;
     bool mine = false;
     if (c1 < C) {
         const long long x = c1 * W / C;
-        locate(a, x, lane, u);
-        mine = u.blk > 0 && x - u.blk + u.nb <= (c1 + 1) * W / C;
+        locate(a, line, x, lane, u);
+        mine = u.blk > 0 && u.blk < u.nb && x - u.blk + u.nb <= (c1 + 1) * W / C;
         c0 = run_of(x - u.blk, W, C);
     }
     grid_dependency_wait();
