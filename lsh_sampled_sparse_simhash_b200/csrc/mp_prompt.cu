@@ -862,6 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // 64 dims at a time through the warp's stage, so that a warp's store covers
             // four whole 128-byte lines and not 16 bytes of 32 (packed prompts 200 -> 184 us)
             const uint32_t stage = ring + kSlots * kTileBytes + warp * kStageBytes;
+            const int r0 = (warp & 3) * 32 + (lane >> 3);  // the first row that this lane stores
+            uint4 *dst = reinterpret_cast<uint4 *>(a.out + (out0 + (4 % G == 0 ? (size_t)(r0 / G) * a.s.Hq + r0 % G : 0)) * kHeadDim) +
+                         (lane & 7);
 #pragma unroll
             for (int c = 0; c < 2; c++) {
                 uint32_t o[64];
@@ -890,8 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                  : "r"(stage + lr * 128 + (((lane & 7) ^ (lr & 7)) << 4))
                                  : "memory");
                     if (rr < rows) {
-                        const size_t at = out0 + (size_t)(rr / G) * a.s.Hq + rr % G;
-                        reinterpret_cast<uint4 *>(a.out + at * kHeadDim)[8 * c + (lane & 7)] = make_uint4(v[0], v[1], v[2], v[3]);
+                        const int at = 4 % G == 0 ? i * (4 / G) * a.s.Hq : (rr / G) * a.s.Hq + rr % G;  // rows of out from dst
+                        dst[(long long)at * (kHeadDim / 8) + 8 * c] = make_uint4(v[0], v[1], v[2], v[3]);
                     }
                 }
                 __syncwarp();
