@@ -346,8 +346,9 @@ typedef struct mp_prompt_shape {
  *        q, k or v
  * Rows of no sequence (behind the last one, say) are neither used nor
  * written; what they hold in q, k and v, NaN included, has no effect.  Within
- * a sequence the values v must be finite: a value that is not reaches the
- * rows before it that share a tile with it.
+ * a sequence a key that is not finite reaches the tokens that see it; the
+ * values v must be finite: one that is not may also reach, in its dim,
+ * up to 255 tokens before it.
  * A weight exp(.) is rounded to bf16 before it multiplies its v (relative
  * 2^-9, about the rounding of out itself); lse comes from the unrounded fp32.
  * status also receives MP_ERR_CUDA if the kernel's internal pipeline stalled

@@ -109,6 +109,32 @@ def test_prompt_moving_maximum(order):
     check_prompt(q, k, v, cu, out, lse)
 
 
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (4, 1), (8, 2)])
+def test_prompt_not_finite(hq, hkv):
+    """A key that is not finite reaches the tokens from its own on; a value that is not, those whose key tiles have it:
+    other kv heads, other sequences and the tokens of earlier tiles are as if they were not there."""
+    lens, g = [300, 129, 200], hq // hkv
+    q, k, v, cu = prompt_case(lens, hq, hkv, seed=140 + hq)
+    want, want_lse = run_prompt(q, k, v, cu)
+    for x in ("nan", "inf", "-inf"):
+        bad = k.clone()
+        bad[cu[0] + 150, 0, 3] = float(x)
+        out, lse = run_prompt(q, bad, v, cu)
+        assert torch.equal(out[:150], want[:150]) and torch.equal(lse[:150], want_lse[:150])
+        assert torch.equal(out[300:], want[300:]) and torch.equal(out[:, g:], want[:, g:])
+    assert not torch.isfinite(run_prompt(q, torch.where(torch.arange(629)[:, None, None] == 150, float("nan"), k.float()).bfloat16(),
+                                         v, cu)[0][150:300].float()).any()
+    bad = v.clone()
+    bad[cu[2] + 128, 0, 9] = float("nan")
+    out, lse = run_prompt(q, k, bad, cu)
+    rest = torch.ones(629, hq, D, dtype=torch.bool)
+    rest[cu[2] + 128:, :g, 9] = False
+    first = 128 // g * 2  # tokens of an item; those whose item begins before the tile may have it as their last one
+    rest[cu[2] + 128 // first * first:cu[2] + 128, :g, 9] = False
+    assert torch.equal(out[rest], want[rest]) and torch.equal(lse, want_lse)
+    assert torch.isnan(out[cu[2] + 128:, :g, 9].float()).all()
+
+
 def test_prompt_bad_lengths_skipped():
     """A sequence whose entries break the rules is skipped and recorded; the others are right."""
     q, k, v, _ = prompt_case([300], 4, 1, seed=8)
