@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
                 const float m = fmaxf(fmaxf(mw[0], mw[1]), fmaxf(mw[2], mw[3]));
 #pragma unroll
                 for (int w = 0; w < kWarps; w++) {
-                    if (mw[w] == -INFINITY) continue;
+                    if (red_ml[w][1][h] == 0.f) continue;  // no token (a sum that is NaN goes on)
                     const float f = ex2(mw[w] - m);
                     const float4 x = *reinterpret_cast<const float4 *>(&acc_at(w, h, 4 * lane));
                     l = fmaf(f, red_ml[w][1][h], l);
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_partials_kernel(const 
         }
 #pragma unroll
         for (int i = 0; i < kMergeBatch; i++)
-            if (ml[i].x != -INFINITY) fold(m, l, v, ml[i].x, ml[i].y, acc[i]);
+            if (ml[i].y != 0.f) fold(m, l, v, ml[i].x, ml[i].y, acc[i]);
     }
     red_v[warp][lane] = v;
     if (lane == 0) {
@@ -568,7 +568,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_partials_kernel(const 
     if (warp != 0) return;
 #pragma unroll
     for (int w = 1; w < kMergeWarps; w++)
-        if (red_m[w] != -INFINITY) fold(m, l, v, red_m[w], red_l[w], red_v[w][lane]);
+        if (red_l[w] != 0.f) fold(m, l, v, red_m[w], red_l[w], red_v[w][lane]);
     const size_t bh = (size_t)u.b * s.Hq + u.kvh * s.G + h;
     const float inv = l == 0.f ? 0.f : 1.f / l;
     reinterpret_cast<float4 *>(a.out + bh * kHeadDim)[lane] = make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);

@@ -323,6 +323,35 @@ def test_paged_bad_pages_left_out():
     check_paged(q, k, v, table, [50, 20], out, lse)
 
 
+@pytest.mark.parametrize("n", [1, 40, 5000])
+def test_paged_not_finite(n):
+    """What is not finite and seen reaches the results of its head, and of no other: a query of NaN, a key, a value."""
+    lens = [n, 77]
+    q, k, v, table = paged_case(lens, 4, 2, 16, seed=75)
+    want, want_lse = run_paged(q, k, v, table, lens)
+    bad = q.clone()
+    bad[0, 1, 5] = float("nan")  # every score of the row
+    out, lse = run_paged(bad, k, v, table, lens)
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(lse[0, 1])
+    rest = [0, 2, 3]
+    assert torch.equal(out[0, rest], want[0, rest]) and torch.equal(out[1], want[1]) and torch.equal(lse[1], want_lse[1])
+    page, row = table[0][(n - 1) // 16], (n - 1) % 16
+    for x in ("nan", "inf"):
+        bad = k.clone()
+        bad[page, 1, row, 7] = float(x)
+        bq = q.clone()
+        bq[0, 2:, 7] = 1.0
+        out, lse = run_paged(bq, bad, v, table, lens)
+        assert torch.isnan(out[0, 2:]).all() and not torch.isfinite(lse[0, 2:]).any()
+        assert torch.equal(out[0, :2], want[0, :2]) and torch.equal(out[1], want[1])
+    bad = v.clone()
+    bad[page, 0, row, 9] = float("nan")
+    out, lse = run_paged(q, k, bad, table, lens)
+    assert torch.isnan(out[0, :2, 9]).all() and torch.equal(lse, want_lse)
+    out[0, :2, 9] = want[0, :2, 9]
+    assert torch.equal(out, want)
+
+
 def test_paged_reads_the_contiguous_cache():
     """The cache of the sampled decode, [B][Hkv][Ncap][d], as one page a sequence: with every token in the exact set
     D the two decodes are the same attention."""
