@@ -304,8 +304,8 @@ int mp_decode_attend_q8(const mp_shape *shape, const void *q, const void *W, con
  * natural logarithms:
  *   out_i = sum_j exp(scale q_i . k_j) v_j / sum_j exp(scale q_i . k_j),
  *   lse_i = log sum_j exp(scale q_i . k_j),
- * over the keys j that query i sees.  A query that sees no key gets out = 0
- * and lse = -inf.  Heads are grouped as everywhere (query head h reads kv head
+ * over the keys j that query i sees.  A query that sees no key, or none whose
+ * score is above -inf, gets out = 0 and lse = -inf.  Heads are grouped as everywhere (query head h reads kv head
  * h / G, G = n_q_heads / n_kv_heads); any G from 1 to 8 is supported.
  * Products are bf16 tensor-core products with fp32 accumulation; maxima, sums
  * and lse are fp32.

@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_after();
             float l0, l1;
             unpair(add2(l[0], l[1]), l0, l1);
-            const float sum = l0 + l1, inv = 1.f / sum;
+            const float sum = l0 + l1, inv = sum == 0.f ? 0.f : 1.f / sum;  // 0: every score is -inf
             // 64 dims at a time through the warp's stage, so that a warp's store covers
             // four whole 128-byte lines and not 16 bytes of 32 (packed prompts 200 -> 184 us)
             const uint32_t stage = ring + kSlots * kTileBytes + warp * kStageBytes;

@@ -135,6 +135,28 @@ def test_prompt_not_finite(hq, hkv):
     assert torch.isnan(out[cu[2] + 128:, :g, 9].float()).all()
 
 
+def test_scores_all_minus_infinity():
+    """Keys of score -inf have no weight; where a query sees no other, its result is that of no key."""
+    lens = [3, 140]
+    q, k, v, cu = prompt_case(lens, 4, 2, seed=150)
+    q[:, :, 5] = 1.0
+    k[cu[1]:cu[1] + 130, 1, 5] = float("-inf")  # of the second sequence's first 130 tokens
+    out, lse = run_prompt(q, k, v, cu)
+    assert (out[3:133, 2:] == 0).all() and (lse[3:133, 2:] == float("-inf")).all()
+    check_prompt(q[133:, 2:], k[133:, 1:], v[133:, 1:], [0, 10], out[133:, 2:], lse[133:, 2:])
+    q, k, v, table = paged_case([33, 2000], 4, 2, 16, seed=151)
+    q[:, :, 5] = 1.0
+    for p in table[1]:
+        if p >= 0:
+            k[p, 1, :, 5] = float("-inf")
+    k[table[0][:2], 1, :, 5] = float("-inf")  # all but its last token
+    out, lse = run_paged(q, k, v, table, [33, 2000])
+    assert (out[1, 2:] == 0).all() and (lse[1, 2:] == float("-inf")).all() and torch.isfinite(out).all()
+    want = v[table[0][2], 1, 0].double()
+    assert ((out[0, 2:].double() - want).abs() <= 2.0 ** -22 * want.abs()).all()  # weight 1 exactly, up to its sum's division
+
+
+
 def test_prompt_bad_lengths_skipped():
     """A sequence whose entries break the rules is skipped and recorded; the others are right."""
     q, k, v, _ = prompt_case([300], 4, 1, seed=8)
