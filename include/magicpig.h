@@ -316,8 +316,8 @@ int mp_decode_attend_q8(const mp_shape *shape, const void *q, const void *W, con
  */
 
 /*
- * Shape of mp_prompt_attend.  Supported: batch >= 1; head_dim == 128;
- * G in 1 .. 8; 0 <= total < 2^25 (so that no wait inside the kernel comes
+ * Shape of mp_prompt_attend.  Supported: 1 <= batch <= 65536; head_dim == 128;
+ * G in 1 .. 8; 0 <= total < 2^25 (both so that no wait inside the kernel comes
  * near its limit of 1 s); strides in elements, multiples of 8 (16 bytes), at
  * least n_heads * head_dim.
  */

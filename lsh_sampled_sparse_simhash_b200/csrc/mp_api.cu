@@ -73,7 +73,7 @@ int validate_prompt_shape(const mp_prompt_shape *in, PromptShape &s)
     int r = validate_heads(s.Hq, s.Hkv, in->head_dim, s.G);
     if (r) return r;
     if (s.Hq > 65535) return MP_ERR_SHAPE;
-    if (s.B < 1 || s.T < 0 || s.T >= (1 << 25)) return MP_ERR_SHAPE;
+    if (s.B < 1 || s.B > 65536 || s.T < 0 || s.T >= (1 << 25)) return MP_ERR_SHAPE;
     if ((r = token_stride(in->q_stride, s.Hq, s.qs)) || (r = token_stride(in->k_stride, s.Hkv, s.ks)) ||
         (r = token_stride(in->v_stride, s.Hkv, s.vs)))
         return r;

@@ -40,6 +40,11 @@ def test_prompt_shapes_refused(lib, bad):
     assert lib.mp_prompt_attend(prompt_shape(**bad), A, A, A, A, A, A, None, None) == mp.MP_ERR_SHAPE
 
 
+def test_prompt_batch_limit(lib):
+    assert lib.mp_prompt_attend(prompt_shape(batch=65537), A, A, A, A, A, A, None, None) == mp.MP_ERR_SHAPE
+    assert lib.mp_prompt_attend(prompt_shape(batch=65536, total=0), None, None, None, A, None, None, None, None) == mp.MP_OK
+
+
 def test_prompt_pointers_refused(lib):
     good = [A, A, A, A, A, A, None, None]
     for i in (0, 1, 2, 3, 4):

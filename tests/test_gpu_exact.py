@@ -78,6 +78,22 @@ def test_prompt_lengths(lens):
     check_prompt(q, k, v, cu, out, lse)
 
 
+@pytest.mark.parametrize("batch,hq,hkv", [(5000, 6, 2), (65536, 2, 1)])
+def test_prompt_many_short_sequences(batch, hq, hkv):
+    """One-token sequences (whose result is their value, exactly), empty ones and a few longer ones among them."""
+    lens = [0 if i % 7 == 3 else 1 for i in range(batch)]
+    longer = {11: 130, batch // 2: 300, batch - 1: 2}
+    for i, n in longer.items():
+        lens[i] = n
+    q, k, v, cu = prompt_case(lens, hq, hkv, seed=160)
+    out, lse = run_prompt(q, k, v, cu)
+    ones = torch.tensor([cu[i] for i, n in enumerate(lens) if n == 1])
+    assert torch.equal(out[ones], v[ones].repeat_interleave(hq // hkv, dim=1))
+    for i, n in longer.items():
+        at = slice(cu[i], cu[i] + n)
+        check_prompt(q[at], k[at], v[at], [0, n], out[at], lse[at])
+
+
 def test_prompt_long():
     """More key tiles than the ring has slots, many times over."""
     q, k, v, cu = prompt_case([2900], 2, 1, seed=5)
