@@ -341,7 +341,8 @@ typedef struct mp_prompt_shape {
  *      three may be parts of one fused projection's rows)
  *   cu_lens  int32 [B + 1] device, 4-byte aligned, not decreasing, from >= 0
  *      to <= T.  A sequence whose two entries break that is skipped and
- *      MP_ERR_CAPACITY recorded.
+ *      MP_ERR_CAPACITY recorded (rows that its neighbours then share get the
+ *      result of either).
  *   out  bf16 [T][Hq][d]     lse  fp32 [T][Hq] (nullable); neither may overlap
  *        q, k or v
  * Rows of no sequence (behind the last one, say) are neither used nor
@@ -414,7 +415,8 @@ int mp_paged_attend(const mp_pages_shape *shape, const void *q, const void *k_pa
  *            apart (0: n_kv_heads * head_dim; else multiples of 8, at least that)
  *   cu_new   int32 [B + 1] device: sequence b has rows [cu_new[b], cu_new[b + 1]);
  *            null: one row for each sequence (n_rows == batch).  Entries as for
- *            cu_lens of mp_prompt_attend, up to n_rows.
+ *            cu_lens of mp_prompt_attend, up to n_rows; if one breaks that, no
+ *            length moves and MP_ERR_CAPACITY is recorded.
  *   advance  nonzero: seq_lens[b] grows by the sequence's rows.  Zero: the
  *            lengths stay (all layers of a model but the last, which share them).
  * The pages must be there (mp_pages_reserve) and no other sequence may hold

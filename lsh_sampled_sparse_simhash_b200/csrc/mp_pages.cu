@@ -591,15 +591,18 @@ __global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(PagesSh
 
 // Moves the lengths after a packed append (its own launch: every row of a
 // sequence reads the old length).  A warp per sequence; a sequence that lacks
-// a page for one of its rows keeps its length.
+// a page for one of its rows keeps its length, and all do if an entry of cu
+// breaks the order (rows that two sequences claim went to one of them).
 __global__ void __launch_bounds__(128) paged_advance_kernel(PagesShape s, const int32_t *cu, int n_rows,
                                                             const int32_t *table, int32_t *lens)
 {
     grid_dependency_wait();
     const int lane = threadIdx.x & 31, b = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (b >= s.B) return;
+    int bad = 0;
+    for (int j = threadIdx.x; j < s.B; j += blockDim.x) bad |= bad_range(cu[j], cu[j + 1], n_rows);
+    if (__syncthreads_or(bad) || b >= s.B) return;
     const int lo = cu[b], hi = cu[b + 1], len = lens[b];
-    if (bad_range(lo, hi, n_rows) || hi == lo || len < 0) return;
+    if (hi == lo || len < 0) return;
     const long long end = (long long)len + (hi - lo);
     if (end > (long long)s.M * s.S) return;
     bool ok = true;

@@ -610,6 +610,18 @@ def test_append_without_pages():
     c.check()
 
 
+@pytest.mark.parametrize("cu", [[0, 6, 4, 9], [0, 6, 9, 10], [-1, 3, 6, 9]])
+def test_append_with_entries_out_of_order(cu):
+    """Rows that two sequences claim, or rows past the last one: recorded, and no sequence grows."""
+    c = Cache(3, 12, 4, 3)
+    assert c.reserve([9, 9, 9])
+    k, v = rand(9, 2, D, seed=5), rand(9, 2, D, seed=6)
+    st = status_word()
+    mp.paged_append(c.shape, k.cuda(), v.cuda(), c.table, c.lens, c.k, c.v, cu_new=i32(cu), status=st)
+    assert st.item() == mp.MP_ERR_CAPACITY and c.lens.tolist() == [0, 0, 0]
+    c.check()
+
+
 def test_append_for_several_layers():
     """advance=False leaves the lengths: two layers share table and lengths; rows come out of a fused projection."""
     c = Cache(2, 8, 16, 3, hkv=3, hq=6)
