@@ -418,7 +418,9 @@ int mp_paged_attend(const mp_pages_shape *shape, const void *q, const void *k_pa
  *            cu_lens of mp_prompt_attend, up to n_rows; if one breaks that, no
  *            length moves and MP_ERR_CAPACITY is recorded.
  *   advance  nonzero: seq_lens[b] grows by the sequence's rows.  Zero: the
- *            lengths stay (all layers of a model but the last, which share them).
+ *            lengths stay (all layers of a model but the last, which share them;
+ *            what such a layer's mp_paged_attend gets as seq_lens is then a copy
+ *            with the new rows added).
  * The pages must be there (mp_pages_reserve) and no other sequence may hold
  * the ones written to.  A row whose page is missing or outside [0, P) is not
  * written, MP_ERR_CAPACITY is recorded, and the length of its sequence stays.

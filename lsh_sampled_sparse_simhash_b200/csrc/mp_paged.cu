@@ -350,6 +350,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     for (int t = 0; t < kStages - 1; t++) issue();
 
     // query fragments of a unit: B of m16n8k16 (k = dims, n = heads), zero for heads past G
+    // (plain loads: this grid may have started before the queries were written, so they are not constant in it)
     uint32_t qf[8][2];
     auto load_q = [&]() {
         const uint16_t *qr = a.q + ((size_t)at.b * s.Hq + at.kvh * s.G + g4) * kHeadDim + t4 * 2;
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
         for (int ks = 0; ks < 8; ks++)
 #pragma unroll
             for (int j = 0; j < 2; j++)
-                qf[ks][j] = g4 < s.G ? __ldg(reinterpret_cast<const uint32_t *>(qr + ks * 16 + j * 8)) : 0u;
+                qf[ks][j] = g4 < s.G ? *reinterpret_cast<const uint32_t *>(qr + ks * 16 + j * 8) : 0u;
     };
     load_q();
 

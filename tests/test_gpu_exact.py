@@ -700,3 +700,68 @@ def test_serving_run():
         torch.cuda.synchronize()
         check_paged(q, c.k.cpu(), c.v.cpu(), c.m.table, c.m.lens, out.cpu(), lse.cpu())
     c.check()
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_serving_step_captured(packed):
+    """A step of two layers (pages, rows and attention of each, lengths at the end) captured once and replayed without
+    a pause: the tokens, pages and results are those of the same calls made one by one."""
+    batch, hq, hkv, size, cols, steps = 5, 8, 2, 16, 9, 40
+    layers, max_len = 2, cols * size
+    shape = mp.PagesShape(batch, hq, hkv, D, batch * cols, size, cols)
+    new = [1, 0, 1, 3, 1] if packed else [1] * batch  # tokens a step
+    n = sum(new)
+    cu = i32([sum(new[:b]) for b in range(batch + 1)]) if packed else None
+    feed = [[rand(n, 2 * hkv, D, seed=700 + 10 * t + i).cuda() for i in range(layers)] for t in range(steps)]
+    asks = [rand(batch, hq, D, seed=2000 + t).cuda() for t in range(steps)]
+
+    def fresh():
+        return dict(table=torch.full((batch, cols), -1, dtype=torch.int32, device="cuda"), lens=i32([0] * batch),
+                    refs=i32([0] * batch * cols), new=i32(new), grown=i32([0] * batch), q=asks[0].clone(), kv=[x.clone() for x in feed[0]],
+                    pools=[[torch.full((batch * cols, hkv, size, D), float("nan"), dtype=torch.bfloat16, device="cuda")
+                            for _ in range(2)] for _ in range(layers)],
+                    out=torch.zeros(layers, batch, hq, D, device="cuda"), lse=torch.zeros(layers, batch, hq, device="cuda"),
+                    ws=torch.empty(mp.paged_workspace_bytes(shape, max_len), dtype=torch.uint8, device="cuda"),
+                    st=status_word())
+
+    def step(c, pause):
+        def then(f, *args, **kw):
+            f(*args, **kw, status=c["st"])
+            if pause:
+                torch.cuda.synchronize()
+        then(mp.pages_reserve, shape, c["new"], c["table"], c["lens"], c["refs"])
+        torch.add(c["lens"], c["new"], out=c["grown"])  # what a layer attends to, its new rows with it
+        for i, (k, v) in enumerate(c["pools"]):
+            then(mp.paged_append, shape, c["kv"][i][:, :hkv], c["kv"][i][:, hkv:], c["table"], c["lens"], k, v, cu_new=cu,
+                 advance=i == layers - 1)
+            then(mp.paged_attend, shape, c["q"], k, v, c["table"], c["grown"], max_len, c["out"][i], c["lse"][i], c["ws"])
+
+    def give(c, t):
+        c["q"].copy_(asks[t])
+        for x, y in zip(c["kv"], feed[t]):
+            x.copy_(y)
+
+    one, rep, results = fresh(), fresh(), []
+    step(fresh(), False)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(rep, False)
+    for t in range(steps):
+        give(rep, t)
+        g.replay()
+        results.append((rep["out"].clone(), rep["lse"].clone(), rep["lens"].clone()))
+    torch.cuda.synchronize()
+    for t in range(steps):
+        give(one, t)
+        step(one, True)
+        for x, y in zip(results[t], (one["out"], one["lse"], one["lens"])):
+            assert torch.equal(x, y), t
+    assert one["st"].item() == 0 and rep["st"].item() == 0
+    lens = [x * steps for x in new]
+    assert one["lens"].tolist() == lens and torch.equal(one["table"], rep["table"]) and torch.equal(one["refs"], rep["refs"])
+    for i, (k, v) in enumerate(one["pools"]):
+        assert torch.equal(torch.nan_to_num(k), torch.nan_to_num(rep["pools"][i][0]))
+        assert torch.equal(torch.nan_to_num(v), torch.nan_to_num(rep["pools"][i][1]))
+    for i, (k, v) in enumerate(one["pools"]):
+        check_paged(asks[-1].cpu(), k.cpu(), v.cpu(), one["table"].tolist(), lens, one["out"][i].cpu(), one["lse"][i].cpu())
