@@ -340,9 +340,8 @@ typedef struct mp_prompt_shape {
  *      by side, tokens q_stride / k_stride / v_stride elements apart (so the
  *      three may be parts of one fused projection's rows)
  *   cu_lens  int32 [B + 1] device, 4-byte aligned, not decreasing, from >= 0
- *      to <= T.  A sequence whose two entries break that is skipped and
- *      MP_ERR_CAPACITY recorded (rows that its neighbours then share get the
- *      result of either).
+ *      to <= T.  The first sequence whose two entries break that and all
+ *      sequences after it are left out and MP_ERR_CAPACITY recorded.
  *   out  bf16 [T][Hq][d]     lse  fp32 [T][Hq] (nullable); neither may overlap
  *        q, k or v
  * Rows of no sequence (behind the last one, say) are neither used nor

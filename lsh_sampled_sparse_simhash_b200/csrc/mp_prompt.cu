@@ -411,12 +411,13 @@ __device__ __forceinline__ int key_tiles(const Item &it, int t, int kTok)
     return first < it.n ? (min(first + kTok, it.n) - 1) / kKeys + 1 : 0;
 }
 
-// Rows of sequence b; a pair of entries that breaks the rules holds none.
+// Rows of sequence b; -1 for a pair of entries that breaks the order or lies
+// outside the rows.
 __device__ __forceinline__ int seq_rows(const Args &a, int b, int &row0)
 {
     const int lo = a.cu[b], hi = a.cu[b + 1];
     row0 = lo;
-    return lo < 0 || hi < lo || hi > a.s.T ? 0 : hi - lo;
+    return lo < 0 || hi < lo || hi > a.s.T ? -1 : hi - lo;
 }
 
 // The place of the k-th set bit of a word (k from 0; there are more than k).
@@ -434,6 +435,8 @@ __device__ __forceinline__ int nth_bit(unsigned bits, int k, int lane)
 // in the (r - F(x + 1))-th sequence that has one.  Ranks are asked for in
 // rising order, so groups only follow, x only falls and the search for the
 // sequence goes on where it was (4096 one-token prompts 2.15 ms -> 0.78 ms).
+// The list ends before the first sequence whose entries break the order: those
+// before it share no row, so all of their items fit the grid and no sum wraps.
 // Run by one warp, rarely and from cold instruction caches, so short code
 // counts: a group of up to 32 sequences is kept in the lanes (packed prompts
 // 168.5 -> 166 us, one short prompt 8.4 -> 7.9; with 64 or 128 kept, more
@@ -444,6 +447,7 @@ struct ItemList {
     int lane;
     int base;            // rank of the group's first item
     int b0, b1, h0, h1;  // sequences and kv heads of the group
+    int end;             // the list goes up to here: B, or the first sequence whose entries break the order
     int heads;           // kv heads a group of this sequence takes
     int x, fx, above;    // F(x) = fx, F(x + 1) = above
     int last;            // rank asked for last
@@ -456,12 +460,15 @@ struct ItemList {
         last = base = b0 = b1 = x = fx = above = seen_b = seen = 0;
         kept = false;
         h0 = h1 = heads = a.s.Hkv;
+        end = a.s.B;
     }
     __device__ __forceinline__ int items(int b) const
     {
         int row0;
         return (seq_rows(a, b, row0) + M - 1) / M;
     }
+    // The list ends before sequence b, the first of the group that breaks the order.
+    __device__ __forceinline__ void cut(int b) { end = b1 = b; }
     __device__ __forceinline__ int F(int y) const
     {
         int f = 0;
@@ -478,14 +485,14 @@ struct ItemList {
             h0 = h1;
             h1 = min(h0 + heads, a.s.Hkv);
         } else {
-            if (b1 >= a.s.B) return false;
+            if (b1 >= end) return false;
             b0 = b1;
             const long long most = kGroupBytes / (2 * 2 * kHeadDim * (long long)a.s.Hkv);  // tokens
             long long sum = 0;
-            if (a.s.T <= most) b1 = a.s.B;  // all of them
-            for (bool open = true; open && b1 < a.s.B;) {
+            if (a.s.T <= most) b1 = end;  // all of them
+            for (bool open = true; open && b1 < end;) {
                 int row0;
-                const int n = b1 + lane < a.s.B ? seq_rows(a, b1 + lane, row0) : 0;
+                const int n = b1 + lane < end ? max(seq_rows(a, b1 + lane, row0), 0) : 0;
                 long long pre = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -495,7 +502,7 @@ struct ItemList {
                 const unsigned over = __ballot_sync(0xffffffffu, sum + pre > most);
                 const int fit = over ? __ffs((int)over) - 1 : 32;
                 if (fit > 0) sum += __shfl_sync(0xffffffffu, pre, fit - 1);
-                b1 = min(b1 + fit, a.s.B);
+                b1 = min(b1 + fit, end);
                 open = fit == 32;
             }
             heads = a.s.Hkv;
@@ -512,9 +519,25 @@ struct ItemList {
         if (kept) {
             n_kept = row_kept = 0;
             if (b0 + lane < b1) n_kept = seq_rows(a, b0 + lane, row_kept);
+            const unsigned bad = __ballot_sync(0xffffffffu, n_kept < 0);
+            if (bad) {
+                cut(b0 + __ffs((int)bad) - 1);
+                if (b0 + lane >= b1) n_kept = 0;
+            }
             most = (n_kept + M - 1) / M;
         } else {
-            for (int b = b0 + lane; b < b1; b += 32) most = max(most, items(b));
+            for (int stop = -1; stop != b1;) {  // a second time without those that do not count
+                if (stop >= 0) cut(stop);
+                stop = b1;
+                most = 0;
+                for (int b = b0 + lane; b < b1; b += 32) {
+                    int row0;
+                    const int n = seq_rows(a, b, row0);
+                    if (n < 0) stop = min(stop, b);
+                    most = max(most, (n + M - 1) / M);
+                }
+                stop = __reduce_min_sync(0xffffffffu, stop);
+            }
         }
         x = __reduce_max_sync(0xffffffffu, most);
         fx = above = 0;
