@@ -68,6 +68,8 @@ constexpr long long kGroupBytes = 32ll << 20;  // K and V of the items in hand: 
 constexpr float kMargin = 24.f;               // log2 units that a score may exceed its row's reference by
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kScale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
+constexpr float kFar = 67108864.f;            // 2^26: a reference of at least this size is kept as the score itself
 
 struct Args {
     PromptShape s;
@@ -331,6 +333,47 @@ __device__ __forceinline__ void publish(uint32_t bar, int lane)
     if (lane == 0) mbar_arrive(bar);
 }
 
+// The reference of a row whose sums may be relative to a score beyond kFar.
+struct Reference {
+    float m;   // log2 units; far: the score
+    float f;   // what the sums so far are multiplied by
+    bool far;
+};
+__device__ __forceinline__ bool is_far(float score) { return fabsf(score) >= kFar && fabsf(score) < INFINITY; }
+
+// The reference after a tile whose largest visible score is `top`, in a warp
+// that has a far one, before or after; far rows' scores become relative to it,
+// in place, and are hidden past lim.  Out of line: it is rare, and a short
+// item's code is mostly run from cold instruction caches (4096 one-token prompts
+// 0.79 ms, with this in line 0.84, without far references 0.75).
+__device__ __noinline__ Reference far_reference(Reference r, float top, int lim, uint32_t s_col)
+{
+    const float lead = r.far ? (top - r.m) * kScale : top * kScale - r.m;
+    r.f = 1.f;
+    if (lead > kMargin) {
+        const bool far = is_far(top);
+        r.f = r.m == -INFINITY ? 0.f
+                               : ex2(fmaf((r.far ? r.m : 0.f) - (far ? top : 0.f), kScale,
+                                          (r.far ? 0.f : r.m) - (far ? 0.f : top * kScale)));
+        r.m = far ? top : top * kScale;
+        r.far = far;
+    }
+    const float base = r.far ? r.m : 0.f;
+#pragma unroll 1
+    for (int k = 0; k < 4; k++) {
+        uint32_t a[32];
+        tmem_ld32(s_col + 32 * k, a);
+        wait_ld();
+        tie32(a);
+        hide(a, lim - 32 * k);
+#pragma unroll
+        for (int i = 0; i < 32; i++) a[i] = __float_as_uint(__uint_as_float(a[i]) - base);
+        tmem_st32(s_col + 32 * k, a);
+    }
+    wait_st();
+    return r;
+}
+
 // A key tile of every row of a warp: P into the columns of S, 64 keys at a
 // time, each half published on its own barrier, the sums into l.  lim: the
 // row's last visible key (masked: some row of the warp does not see all).
@@ -339,12 +382,16 @@ __device__ __forceinline__ void publish(uint32_t bar, int lane)
 // comes near fp32's range); past that, or with no reference yet, the tile's
 // maximum takes its place and l and O are rescaled (`o_used`: O holds
 // something; all products into it are complete, as they were issued before
-// this S).  Scores are read twice from TMEM, through three buffers of 32: all
-// 128 at once spill.
-__device__ __forceinline__ void row_tile(float &m, uint64_t *l, int lim, bool masked, bool o_used, uint32_t s_col,
+// this S).  A weight is 2^(s kScale - m), one multiply-add a score; m is a
+// rounded product, so all weights and sums of a row share a factor of up to
+// 2^(half a unit in the last place of m), which would leave fp32's range for
+// scores past 2^33.  So a reference beyond kFar is kept as the score itself
+// (`far`), and every score of the row is taken relative to it first.  Scores
+// are read twice from TMEM, through three buffers of 32: all 128 at once spill.
+__device__ __forceinline__ void row_tile(float &m, bool &far, uint64_t *l, int lim, bool masked, bool o_used, uint32_t s_col,
                                          uint32_t o_col, uint32_t p_bar, int lane)
 {
-    const float scale = kLog2e * 0.08838834764831845f;  // log2(e) / sqrt(128)
+    const float scale = kScale;
     uint32_t a[32], b[32], c[32];
     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -361,11 +408,24 @@ __device__ __forceinline__ void row_tile(float &m, uint64_t *l, int lim, bool ma
         row_max(a, mx);
         row_max(b, mx);
     }
-    const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * scale;
+    const float raw = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]), top = raw * scale;
     const bool grow = top > m + kMargin;
-    if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
-        if (grow) m = top;
+    if (__any_sync(0xffffffffu, grow || far)) {
+        float f = 1.f;
+        if (__any_sync(0xffffffffu, far || is_far(raw))) {
+            const Reference r = far_reference(Reference{m, 1.f, far}, raw, lim, s_col);
+            m = r.m;
+            f = r.f;
+            far = r.far;
+            tmem_ld32(s_col, a);
+            tmem_ld32(s_col + 32, b);
+            wait_ld();
+            tie32(a);
+            tie32(b);
+        } else if (grow) {
+            f = m == -INFINITY ? 0.f : ex2(m - top);
+            m = top;
+        }
         l[0] = fma2(l[0], pair(f, f), 0ull);
         l[1] = fma2(l[1], pair(f, f), 0ull);
         if (o_used) {
@@ -380,7 +440,7 @@ __device__ __forceinline__ void row_tile(float &m, uint64_t *l, int lim, bool ma
             }
         }
     }
-    const float neg = m == -INFINITY ? 0.f : -m;
+    const float neg = far || m == -INFINITY ? 0.f : -m;
     const uint64_t scale2 = pair(scale, scale), ms = pair(neg, neg);
     tmem_ld32(s_col + 64, c);
     weights(a, scale2, ms, l, s_col);
@@ -898,6 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             }
             float m = -INFINITY;
+            bool far = false;
             uint64_t l[2] = {0ull, 0ull};  // four partial sums
             bool ok = true;
             for (int kt = nt - 1; kt >= 0 && ok; kt--, par ^= 1u) {
@@ -906,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 fence_after();
                 const int lim = limit - kt * kKeys;
                 const bool masked = __any_sync(0xffffffffu, lim < kKeys - 1);
-                row_tile(m, l, lim, masked, kt < nt - 1, s_col, o_col, bar(B_P + 2 * t), lane);
+                row_tile(m, far, l, lim, masked, kt < nt - 1, s_col, o_col, bar(B_P + 2 * t), lane);
             }
             if (!ok) break;
             live = walk.next(it);  // while the last product runs
@@ -956,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             }
-            if (a.lse && r < rows) a.lse[out0 + (size_t)(r / G) * a.s.Hq + r % G] = (m + log2f(sum)) * kLn2;
+            if (a.lse && r < rows) a.lse[out0 + (size_t)(r / G) * a.s.Hq + r % G] = ((far ? m * kScale : m) + log2f(sum)) * kLn2;
         }
     }
     fence_before();

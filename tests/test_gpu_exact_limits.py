@@ -52,3 +52,26 @@ def test_prompt_out_of_order_ends_the_list(total, hq, hkv, cu, good):
         at = slice(u * g, (u + 1) * g)
         check_prompt(q[:, at], k[:, u:u + 1], v[:, u:u + 1], cu[:good + 1], out[:, at], lse[:, at])
     assert (lse[:end] != 7.0).all() and (lse[end:] == 7.0).all() and (out[end:] == 7.0).all()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("power", [5, 6, 9, 12, 20, 45])
+def test_prompt_scores_of_any_size(power, sign):
+    """Scores up to 2^100, so far apart that one key has all the weight: each row's result is the value of the visible
+    key with the largest score.  (At power 6 a row's scores lie on both sides of 2^24.)"""
+    n, hq, hkv = 512, 4, 2
+    order = torch.randperm(n, generator=torch.Generator().manual_seed(power))
+    w = (128 + torch.arange(n) % 128) * 2 ** (torch.arange(n) // 128)  # 512 different numbers of 8 bits
+    w = w[order].double()
+    q = torch.full((n, hq, D), sign * 2.0 ** power, dtype=torch.bfloat16)
+    k = (w * 2.0 ** power).bfloat16()[:, None, None].expand(n, hkv, D).contiguous()
+    v = rand(n, hkv, D, seed=300)
+    s = sign * w * 2.0 ** (2 * power) * 128  # exact, in fp32 too
+    out, lse = run_prompt(q, k, v, [0, n])
+    best = torch.stack([s[:i + 1].argmax() for i in range(n)])
+    want = v[best].repeat_interleave(hq // hkv, dim=1).double()
+    # the weight is rounded to bf16 against an unrounded sum, and the result to bf16
+    assert ((out.double() - want).abs() <= (2 * 2.0 ** -8 + 2.0 ** -16) * want.abs() + 1e-30).all()
+    want = s[best][:, None] / 128 ** 0.5
+    # one product, one multiply-add and the conversion to natural logarithms, with rounded constants; a logarithm of the sum
+    assert ((lse.double() - want).abs() <= 6 * 2.0 ** -24 * want.abs() + 2.0 ** -22).all()
