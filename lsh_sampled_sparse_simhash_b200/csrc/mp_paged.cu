@@ -284,12 +284,14 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
     // The table entry of the next tile is fetched a tile ahead of its copies:
     // lane i < 16 holds that of token i (ALIGNED: all lanes the tile's one).
     int tok0 = 0, page = -1, off_pg = 0;  // off_pg: the token's row in its page
+    bool inside = false;                  // the token is one of the sequence's
     auto fetch = [&]() {
         if (rd.left <= 0) return;
         tok0 = (rd.blk * kWarps + warp) * kTile;
         const int tok = ALIGNED ? tok0 : tok0 + (lane & 15);
         const int col = page_of(a, tok, off_pg);
-        page = tok < rd.len ? a.table[(size_t)rd.b * s.M + col] : -2;
+        inside = tok < rd.len;
+        page = inside ? a.table[(size_t)rd.b * s.M + col] : -1;
         if (rd.blk == 0 && lane < 2 * s.G)  // a unit begins: its queries (2 lines a head) into L1
             asm volatile("prefetch.global.L1 [%0];" ::"l"(
                 a.q + ((size_t)rd.b * s.Hq + rd.kvh * s.G) * kHeadDim + lane * 64));
@@ -303,7 +305,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) paged_attend_kernel
         if (rd.left > 0) {
             const uint32_t dst = my_ring + (uint32_t)(slot_rd * kTileBytes);
             const bool good = page >= 0 && page < s.P;
-            if (!good && page != -2) set_status(a.status, MP_ERR_CAPACITY);
+            if (!good && inside) set_status(a.status, MP_ERR_CAPACITY);
             const int p = lane & 15, r0 = lane >> 4;
             unsigned seen;
             if (ALIGNED) {

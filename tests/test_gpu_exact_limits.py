@@ -75,3 +75,20 @@ def test_prompt_scores_of_any_size(power, sign):
     want = s[best][:, None] / 128 ** 0.5
     # one product, one multiply-add and the conversion to natural logarithms, with rounded constants; a logarithm of the sum
     assert ((lse.double() - want).abs() <= 6 * 2.0 ** -24 * want.abs() + 2.0 ** -22).all()
+
+
+# -------------------------------------------------------------------- paged ----
+
+@pytest.mark.parametrize("size", [16, 24])
+@pytest.mark.parametrize("bad", [-1, -2, -7, -(1 << 31), "P"])
+def test_paged_reports_every_bad_page(size, bad):
+    """Any number outside the pool within a length: left out and recorded; behind the length it does not matter."""
+    lens = [100, 40]
+    q, k, v, table = paged_case(lens, 4, 2, size, seed=330)
+    bad = k.shape[0] if bad == "P" else bad
+    table[1] = table[1][:2] + [bad] * (len(table[1]) - 2) if size == 24 else table[1][:3] + [bad] * (len(table[1]) - 3)
+    out, lse = run_paged(q, k, v, table, lens)
+    check_paged(q, k, v, table, lens, out, lse)
+    table[0][1] = bad
+    out, lse = run_paged(q, k, v, table, lens, want=mp.MP_ERR_CAPACITY)
+    check_paged(q, k, v, table, lens, out, lse)
