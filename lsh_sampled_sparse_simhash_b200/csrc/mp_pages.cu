@@ -586,7 +586,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) paged_append_kernel(PagesSh
             }
         }
     }
-    if (!cu && advance && lane == 0) lens[b] = len + 1;  // this warp alone reads and writes it
+    if (!cu && advance) {
+        __syncwarp();  // every lane has read the length
+        if (lane == 0) lens[b] = len + 1;  // this warp alone reads and writes it
+    }
 }
 
 // Moves the lengths after a packed append (its own launch: every row of a

@@ -92,3 +92,21 @@ def test_paged_reports_every_bad_page(size, bad):
     table[0][1] = bad
     out, lse = run_paged(q, k, v, table, lens, want=mp.MP_ERR_CAPACITY)
     check_paged(q, k, v, table, lens, out, lse)
+
+
+def test_append_one_row_of_every_sequence():
+    """The largest batch, one row each, step after step: every row in its place, every length one more."""
+    batch, size, steps = 4096, 4, 6
+    shape = mp.PagesShape(batch, 1, 1, D, 2 * batch, size, 2)
+    table, lens, refs = i32([[-1] * 2] * batch), i32([0] * batch), i32([0] * 2 * batch)
+    k, v = (torch.zeros(2 * batch, 1, size, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    mp.pages_reserve(shape, i32([steps] * batch), table, lens, refs)
+    rows = [(rand(batch, 1, D, seed=340 + t), rand(batch, 1, D, seed=360 + t)) for t in range(steps)]
+    st = status_word()
+    for a, b in rows:
+        mp.paged_append(shape, a.cuda(), b.cuda(), table, lens, k, v, status=st)
+    assert st.item() == 0 and (lens == steps).all()
+    at = table.cpu().long()
+    for t, (a, b) in enumerate(rows):
+        assert torch.equal(k.cpu()[at[:, t // size], 0, t % size], a[:, 0])
+        assert torch.equal(v.cpu()[at[:, t // size], 0, t % size], b[:, 0])
