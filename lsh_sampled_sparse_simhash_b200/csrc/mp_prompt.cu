@@ -752,7 +752,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     next_block(smem_u32(&next_sh), bar(B_NEXT));
                 }
                 __syncwarp();
-                if (!wwait(B_NEXT, (k - 1) & 1)) break;
+                if (!wwait(B_NEXT, (k - 1) & 1)) {
+                    wait_teardown(bar(B_NEXT), (k - 1) & 1);  // the answer lands before the block leaves
+                    break;
+                }
                 more = block_taken(smem_u32(&next_sh), r);
                 __syncwarp();
             }
