@@ -77,6 +77,36 @@ def test_prompt_scores_of_any_size(power, sign):
     assert ((lse.double() - want).abs() <= 6 * 2.0 ** -24 * want.abs() + 2.0 ** -22).all()
 
 
+@pytest.mark.parametrize("threads", [1])
+def test_first_calls_of_threads(threads):
+    """A process whose first call comes from a new host thread."""
+    code = f'''
+import threading, torch
+import lsh_sampled_sparse_simhash_b200 as mp
+N = {threads}
+q = torch.ones(8, 4, 128, dtype=torch.bfloat16, device="cuda")
+cu = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+outs = [torch.zeros_like(q) for _ in range(N)]
+torch.cuda.synchronize()
+mp.library()
+ready, failed = threading.Barrier(N), []
+def call(i):
+    ready.wait()
+    try:
+        mp.prompt_attend(mp.PromptShape(1, 4, 4, 128, 8), q, q, q, cu, outs[i])
+    except Exception as e:
+        failed.append(e)
+threads = [threading.Thread(target=call, args=(i,)) for i in range(N)]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+assert not failed, failed
+assert all((o == 1).all() for o in outs)
+'''
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # -------------------------------------------------------------------- paged ----
 
 @pytest.mark.parametrize("size", [16, 24])
