@@ -77,9 +77,9 @@ def test_prompt_scores_of_any_size(power, sign):
     assert ((lse.double() - want).abs() <= 6 * 2.0 ** -24 * want.abs() + 2.0 ** -22).all()
 
 
-@pytest.mark.parametrize("threads", [1])
+@pytest.mark.parametrize("threads", [1, 8])
 def test_first_calls_of_threads(threads):
-    """A process whose first call comes from a new host thread."""
+    """A process whose first call comes from a new host thread, or from eight at once."""
     code = f'''
 import threading, torch
 import lsh_sampled_sparse_simhash_b200 as mp
