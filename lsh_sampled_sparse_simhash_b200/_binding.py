@@ -271,6 +271,17 @@ def decode_attend_q8(shape: Shape, q, W, codes, k8, v_cache, seq_lens, max_len: 
 
 # ---- exact attention: prompts and the paged cache (include/magicpig.h) ----
 
+def _i32(n: int, what: str) -> int:
+    """n, refused where the library's 32-bit argument does not hold it (ctypes keeps the low bits without a word)."""
+    if not -1 << 31 <= n < 1 << 31:
+        raise ValueError(f"{what}: {n} does not fit 32 bits")
+    return n
+
+
+def _fields32(shape):
+    """A shape's fields, in order, each checked by _i32."""
+    return [_i32(getattr(shape, f.name), f.name) for f in dataclasses.fields(shape)]
+
 @dataclasses.dataclass(frozen=True)
 class PromptShape:
     """Shape of packed prompts (see mp_prompt_shape; the strides come from the tensors)."""
@@ -279,6 +290,9 @@ class PromptShape:
     n_kv_heads: int
     head_dim: int
     total: int
+
+    def __post_init__(self):
+        _fields32(self)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -296,8 +310,7 @@ class PagesShape:
         # frozen, so the C struct and the tensors' shapes are made once
         def put(name, value):
             object.__setattr__(self, name, value)
-        put("_c", _CPagesShape(self.batch, self.n_q_heads, self.n_kv_heads, self.head_dim, self.n_pages,
-                               self.page_size, self.max_pages))
+        put("_c", _CPagesShape(*_fields32(self)))
         put("_ref", ctypes.byref(self._c))
         put("_pool", (self.n_pages, self.n_kv_heads, self.page_size, self.head_dim))
         put("_table", (self.batch, self.max_pages))
@@ -327,7 +340,7 @@ def _rows_arg(t, what: str, dtype, shape, device: int):
     s0, s1, s2 = t.stride()
     if rows and (s2 != 1 or (heads > 1 and s1 != d)) or rows > 1 and s0 < heads * d:
         _refuse(t, what, dtype, shape, device)
-    return t.data_ptr(), s0 if rows > 1 else 0  # (0 is "side by side" to the library)
+    return t.data_ptr(), _i32(s0, f"{what}: token stride") if rows > 1 else 0  # (0 is "side by side" to the library)
 
 
 def _opt(t, what: str, dtype, shape, device: int) -> Optional[int]:
@@ -353,7 +366,8 @@ def prompt_attend(shape: PromptShape, q, k, v, cu_lens, out, lse=None, status=No
 
 def paged_workspace_bytes(shape: PagesShape, max_len: int) -> int:
     n = ctypes.c_size_t()
-    _check(library().mp_paged_workspace_bytes(shape._ref, int(max_len), ctypes.byref(n)), "mp_paged_workspace_bytes")
+    _check(library().mp_paged_workspace_bytes(shape._ref, _i32(int(max_len), "max_len"), ctypes.byref(n)),
+           "mp_paged_workspace_bytes")
     return n.value
 
 
@@ -368,7 +382,7 @@ def paged_attend(shape: PagesShape, q, k_pages, v_pages, page_table, seq_lens, m
                                      _arg(k_pages, "k_pages", bf16, shape._pool, dev),
                                      _arg(v_pages, "v_pages", bf16, shape._pool, dev),
                                      _arg(page_table, "page_table", i32, shape._table, dev),
-                                     _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev), int(max_len),
+                                     _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev), _i32(int(max_len), "max_len"),
                                      _arg(out, "out", f32, shape._q, dev), _arg(lse, "lse", f32, shape._q[:2], dev),
                                      _arg(workspace, "workspace", workspace.dtype, workspace.shape, dev),
                                      workspace.numel() * workspace.element_size(),
@@ -381,7 +395,7 @@ def paged_append(shape: PagesShape, k_new, v_new, page_table, seq_lens, k_pages,
     or rows [cu_new[b], cu_new[b+1]) for sequence b (cu_new int32 [B+1]).  advance: seq_lens grow."""
     import torch
     dev, bf16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
-    rows = (k_new.shape[0], shape.n_kv_heads, shape.head_dim)
+    rows = (_i32(k_new.shape[0], "rows of k_new"), shape.n_kv_heads, shape.head_dim)
     knp, ks = _rows_arg(k_new, "k_new", bf16, rows, dev)
     vnp, vs = _rows_arg(v_new, "v_new", bf16, rows, dev)
     _check(library().mp_paged_append(shape._ref, knp, vnp, ks, vs, _opt(cu_new, "cu_new", i32, (shape.batch + 1,), dev),
@@ -407,7 +421,7 @@ def pages_fork(shape: PagesShape, src, dst, page_table, seq_lens, refs, copies, 
     """Makes sequence dst[i] a copy of src[i] (int32 [n] both); copies int32 [1+n,4] receives the page copies that
     pages_copy has to make in every layer's pools."""
     import torch
-    dev, i32, n = torch.cuda.current_device(), torch.int32, src.numel()
+    dev, i32, n = torch.cuda.current_device(), torch.int32, _i32(src.numel(), "entries of src")
     _check(library().mp_pages_fork(shape._ref, _arg(src, "src", i32, (n,), dev), _arg(dst, "dst", i32, (n,), dev), n,
                                    _arg(page_table, "page_table", i32, shape._table, dev),
                                    _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev),
@@ -419,7 +433,7 @@ def pages_fork(shape: PagesShape, src, dst, page_table, seq_lens, refs, copies, 
 def pages_free(shape: PagesShape, seqs, page_table, seq_lens, refs, status=None, stream=None):
     """Ends the sequences seqs (int32 [n]): their pages lose a count, their rows become -1, their lengths 0."""
     import torch
-    dev, i32, n = torch.cuda.current_device(), torch.int32, seqs.numel()
+    dev, i32, n = torch.cuda.current_device(), torch.int32, _i32(seqs.numel(), "entries of seqs")
     _check(library().mp_pages_free(shape._ref, _arg(seqs, "seqs", i32, (n,), dev), n,
                                    _arg(page_table, "page_table", i32, shape._table, dev),
                                    _arg(seq_lens, "seq_lens", i32, (shape.batch,), dev),
@@ -442,7 +456,7 @@ def pages_copy(shape: PagesShape, copies, k_pages, v_pages, status=None, stream=
     """Copies pages within one layer's pools: copies int32 [1+n,4], entry 0 {count,0,0,0}, then {src, dst, rows, 0}."""
     import torch
     dev, bf16, i32 = torch.cuda.current_device(), torch.bfloat16, torch.int32
-    n = copies.shape[0]
+    n = _i32(copies.shape[0], "entries of copies")
     _check(library().mp_pages_copy(shape._ref, _arg(copies, "copies", i32, (n, 4), dev), n - 1,
                                    _arg(k_pages, "k_pages", bf16, shape._pool, dev),
                                    _arg(v_pages, "v_pages", bf16, shape._pool, dev),
