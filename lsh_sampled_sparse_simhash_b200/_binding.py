@@ -316,6 +316,9 @@ class PagesShape:
         put("_table", (self.batch, self.max_pages))
         put("_q", (self.batch, self.n_q_heads, self.head_dim))
 
+    def __reduce__(self):  # the C struct is made anew where a copy or a pickle arrives
+        return PagesShape, dataclasses.astuple(self)
+
     def c(self) -> _CPagesShape:
         return self._c
 

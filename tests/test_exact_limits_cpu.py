@@ -1,4 +1,7 @@
 """Exact attention and the paged cache, host side only: arguments at the limits of what the binding passes on."""
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -40,3 +43,13 @@ def test_shapes_past_32_bits_refused():
     for name in good:
         with pytest.raises(ValueError, match=name):
             mp.PromptShape(**{**good, name: (1 << 32) + good[name]})
+
+
+@pytest.mark.parametrize("shape", [mp.PromptShape(2, 8, 2, 128, 100), mp.PagesShape(2, 8, 2, 128, 10, 16, 5)])
+def test_shapes_copied_and_pickled(shape):
+    """A server sends its shapes to other processes."""
+    for other in (copy.copy(shape), copy.deepcopy(shape), pickle.loads(pickle.dumps(shape))):
+        assert other == shape and hash(other) == hash(shape)
+    if isinstance(shape, mp.PagesShape):
+        other = pickle.loads(pickle.dumps(shape))
+        assert mp.paged_workspace_bytes(other, 80) == mp.paged_workspace_bytes(shape, 80) > 0
