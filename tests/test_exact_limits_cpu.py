@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import lsh_sampled_sparse_simhash_b200 as mp
+from exact_ref import attend, check_head, check_paged, check_prompt
 from lsh_sampled_sparse_simhash_b200 import _binding as B
 
 NO_DEVICE = -1  # what get_device() says of a tensor without memory
@@ -53,3 +54,27 @@ def test_shapes_copied_and_pickled(shape):
     if isinstance(shape, mp.PagesShape):
         other = pickle.loads(pickle.dumps(shape))
         assert mp.paged_workspace_bytes(other, 80) == mp.paged_workspace_bytes(shape, 80) > 0
+
+
+@pytest.mark.parametrize("wrong", [float("nan"), float("inf"), float("-inf"), 0.01, -0.01])
+def test_checks_refuse_a_wrong_lse(wrong):
+    """The checks that the GPU tests rely on accept the reference's own lse, and no other beside right results."""
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (torch.randn(20, 1, 128, generator=g).bfloat16() for _ in range(3))
+    seen = torch.arange(1, 21)
+    ref = attend(q[:, 0], k[:, 0], v[:, 0], seen)
+    out, lse = ref[0].bfloat16()[:, None], ref[1].float()[:, None]
+    bad = lse.clone()
+    bad[7] += wrong
+    check_head(out[:, 0], lse[:, 0], ref, seen, True)
+    check_prompt(q, k, v, [0, 20], out, lse)
+    with pytest.raises(AssertionError):
+        check_head(out[:, 0], bad[:, 0], ref, seen, True)
+    with pytest.raises(AssertionError):
+        check_prompt(q, k, v, [0, 20], out, bad)
+    pools = [x.transpose(0, 1)[None].contiguous() for x in (k, v)]  # one page of 20 tokens
+    one = attend(q[:1, 0], k[:, 0], v[:, 0], torch.tensor([20]))
+    out, lse = one[0].float()[None], one[1].float()[None]
+    check_paged(q[:1], *pools, [[0]], [20], out, lse)
+    with pytest.raises(AssertionError):
+        check_paged(q[:1], *pools, [[0]], [20], out, lse + wrong)
