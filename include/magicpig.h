@@ -317,9 +317,10 @@ int mp_decode_attend_q8(const mp_shape *shape, const void *q, const void *W, con
 
 /*
  * Shape of mp_prompt_attend.  Supported: 1 <= batch <= 65536; head_dim == 128;
- * G in 1 .. 8; 0 <= total < 2^25 (both so that no wait inside the kernel comes
- * near its limit of 1 s); strides in elements, multiples of 8 (16 bytes), at
- * least n_heads * head_dim.
+ * G in 1 .. 8; 0 <= total < 2^25 (both bound the waits inside the kernel: the
+ * longest, for the last tokens of a sequence of that length, takes 0.4 to 0.7 s
+ * of the 4 s after which it gives up); strides in elements, multiples of 8 (16
+ * bytes), at least n_heads * head_dim.
  */
 typedef struct mp_prompt_shape {
     int32_t batch;      /* B: sequences in the batch */

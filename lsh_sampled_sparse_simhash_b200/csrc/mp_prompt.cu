@@ -41,8 +41,11 @@
 // polynomial (within 2%: the power cap), all 128 scores of a row in registers
 // (within 1%).
 //
-// Every wait is bounded (1 s); on expiry MP_ERR_CUDA is recorded and the block
-// winds down, waiting for its copies and products in flight.
+// Every wait is bounded (4 s, as a role may wait for a whole item of the others:
+// 262144 rounds for the last of 2^25 tokens, 0.41 s at 1965 MHz and 0.69 s at the
+// 1185 MHz of a long run under the power cap); on expiry MP_ERR_CUDA is recorded
+// and the block winds down, waiting (1 s each) for its copies and products in
+// flight.
 #include <cuda.h>
 #include <math.h>
 
@@ -95,13 +98,14 @@ enum {
     kBars = B_END + 1
 };
 constexpr int kRoles = 8 + 3;  // warps that read an item
+constexpr unsigned long long kItemWaitNs = 4 * kWaitLimitNs;
 
 __device__ __noinline__ bool wait_slow(uint32_t a, uint32_t parity, volatile int *abort_flag, int32_t *status)
 {
     const uint64_t t0 = globaltimer();
     while (!mbar_try_wait(a, parity)) {
         if (*abort_flag) return false;
-        if (globaltimer() - t0 > kWaitLimitNs) {
+        if (globaltimer() - t0 > kItemWaitNs) {
             *abort_flag = 1;
             set_status(status, MP_ERR_CUDA);
             return false;
