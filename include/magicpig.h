@@ -308,7 +308,9 @@ int mp_decode_attend_q8(const mp_shape *shape, const void *q, const void *W, con
  * score is above -inf, gets out = 0 and lse = -inf.  Heads are grouped as everywhere (query head h reads kv head
  * h / G, G = n_q_heads / n_kv_heads); any G from 1 to 8 is supported.
  * Products are bf16 tensor-core products with fp32 accumulation; maxima, sums
- * and lse are fp32.
+ * and lse are fp32.  Values v may be up to 2^78 in size: before the division the
+ * sums hold up to 2^25 of them with weights of up to 2^24 (prompts; 2^30 and 2^8
+ * in the decode).
  *
  * Each `status` below is a nullable int32 device word, 4-byte aligned, that
  * is written only when the call finds something wrong on the device (so the

@@ -77,6 +77,24 @@ def test_prompt_scores_of_any_size(power, sign):
     assert ((lse.double() - want).abs() <= 6 * 2.0 ** -24 * want.abs() + 2.0 ** -22).all()
 
 
+@pytest.mark.parametrize("lag", [0.0, 15.0])
+def test_values_up_to_their_limit(lag):
+    """Values of 2^78: the results of the same values without the factor, times it, exactly.  With a lag the rows' scores
+    rise by that much (e^15 = 2^21.6) behind the first key tile that they meet."""
+    n = 900
+    q, k, v, cu = prompt_case([n], 4, 2, seed=310)
+    q[:, :, 0], k[:, :, 0] = 1.0, 0.0
+    k[:n - 200, :, 0] = lag * 128 ** 0.5
+    want, want_lse = run_prompt(q, k, v, cu)
+    out, lse = run_prompt(q, k, (v.float() * 2.0 ** 78).bfloat16(), cu)
+    assert torch.equal(out.double(), want.double() * 2.0 ** 78) and torch.equal(lse, want_lse)
+    check_prompt(q, k, v, cu, want, want_lse)
+    q, k, v, table = paged_case([n, 5], 4, 2, 16, seed=311)
+    want, want_lse = run_paged(q, k, v, table, [n, 5])
+    out, lse = run_paged(q, k, (v.float() * 2.0 ** 78).bfloat16(), table, [n, 5])
+    assert torch.equal(out.double(), want.double() * 2.0 ** 78) and torch.equal(lse, want_lse)
+
+
 @pytest.mark.parametrize("threads", [1, 8])
 def test_first_calls_of_threads(threads):
     """A process whose first call comes from a new host thread, or from eight at once."""
