@@ -95,6 +95,30 @@ def test_values_up_to_their_limit(lag):
     assert torch.equal(out.double(), want.double() * 2.0 ** 78) and torch.equal(lse, want_lse)
 
 
+@pytest.mark.parametrize("hq,hkv,lens", [
+    (16, 16, [1500, 0, 1800, 700, 900, 3000, 1, 0, 2500, 40]),  # groups of up to 4096 tokens
+    (16, 16, [300, 0, 5000, 1, 900, 0]),                        # one longer than a group: 13 kv heads, then 3
+    (16, 8, [50] * 60 + [9000] + [20] * 40 + [0, 129]),         # more than 32 sequences to a group, before and behind it
+    (32, 16, [4096, 4096, 4097, 1]),
+])
+def test_prompt_groups_of_sequences(hq, hkv, lens):
+    """More keys and values than the blocks keep together: every row is written, with the result of a call for its sequence
+    alone; the longest sequence and some heads against the 64-bit reference."""
+    q, k, v, cu = prompt_case(lens, hq, hkv, pad=3, seed=320)
+    out, lse, status = attend_rows(q, k, v, cu)
+    assert status == 0 and (lse[:cu[-1]] != 7.0).all() and (lse[cu[-1]:] == 7.0).all() and (out[cu[-1]:] == 7.0).all()
+    for lo, n in zip(cu, lens):
+        if n:
+            at = slice(lo, lo + n)
+            alone, alone_lse, _ = attend_rows(q[at], k[at], v[at], [0, n])
+            assert torch.equal(out[at], alone) and torch.equal(lse[at], alone_lse), (lo, n)
+    g, lo = hq // hkv, cu[lens.index(max(lens))]
+    at = slice(lo, lo + max(lens))
+    for u in (0, hkv - 1):  # of the first part of the heads and of the second
+        h = u * g
+        check_prompt(q[at, h:h + 1], k[at, u:u + 1], v[at, u:u + 1], [0, max(lens)], out[at, h:h + 1], lse[at, h:h + 1])
+
+
 @pytest.mark.parametrize("threads", [1, 8])
 def test_first_calls_of_threads(threads):
     """A process whose first call comes from a new host thread, or from eight at once."""
@@ -158,3 +182,111 @@ def test_append_one_row_of_every_sequence():
     for t, (a, b) in enumerate(rows):
         assert torch.equal(k.cpu()[at[:, t // size], 0, t % size], a[:, 0])
         assert torch.equal(v.cpu()[at[:, t // size], 0, t % size], b[:, 0])
+
+
+def test_plans_of_a_large_pool():
+    """A pool whose runs are longer than the plans keep in registers (1024 pages a warp): reserve, fork, free and compact
+    with used and free pages all over it, against the model."""
+    P, batch, cols, size = 300000, 60, 3000, 4
+    shape = mp.PagesShape(batch, 4, 1, D, P, size, cols)
+    r = random.Random(1)
+    m = Pages(batch, P, size, cols)
+    order = r.sample(range(P), P)
+    at = 0
+    for b in range(40):
+        n = r.randint(1, 2400 * size)
+        h = -(-n // size)
+        m.table[b] = order[at:at + h] + [-1] * (cols - h)
+        m.lens[b] = n
+        at += h
+    for row in m.table:
+        for p in row:
+            if p >= 0:
+                m.refs[p] = 1
+    for p in order[at:at + 200000]:  # pages of nobody's here
+        m.refs[p] = 2
+    table, lens, refs = i32(m.table), i32(m.lens), i32(m.refs)
+    st = status_word()
+
+    def same():
+        torch.cuda.synchronize()
+        assert st.item() == 0 and lens.tolist() == m.lens and refs.tolist() == m.refs and table.tolist() == m.table
+
+    def entries(copies, want):
+        got = copies.tolist()
+        assert got[0] == [len(want), 0, 0, 0] and [tuple(e[:3]) for e in got[1:1 + len(want)]] == want
+
+    same()
+    new = [r.choice((0, 1, 9, 2000)) if b < 40 else 0 for b in range(batch)]
+    assert m.reserve(new)
+    mp.pages_reserve(shape, i32(new), table, lens, refs, status=st)
+    same()
+    src, dst = [r.randrange(40) for _ in range(20)], list(range(40, 60))
+    copies = torch.zeros(21, 4, dtype=torch.int32, device="cuda")
+    mp.pages_fork(shape, i32(src), i32(dst), table, lens, refs, copies, status=st)
+    entries(copies, m.fork(src, dst))
+    same()
+    ends = list(range(0, 60, 3))
+    m.free(ends)
+    mp.pages_free(shape, i32(ends), table, lens, refs, status=st)
+    same()
+    copies = torch.zeros(1 + P // 2, 4, dtype=torch.int32, device="cuda")
+    mp.pages_compact(shape, table, refs, copies, status=st)
+    entries(copies, m.compact())
+    same()
+    new = [4000 if t[0] < 0 else 0 for t in m.table]
+    assert m.reserve(new)
+    mp.pages_reserve(shape, i32(new), table, lens, refs, status=st)
+    same()
+
+
+def test_fork_with_too_few_pages_changes_nothing():
+    c = Cache(6, 10, 4, 6)
+    assert c.reserve([6, 0, 0, 3, 0, 0])
+    c.append([6, 0, 0, 3, 0, 0])
+    assert c.reserve([18, 0, 0, 9, 0, 0]) and len(c.m.free_pages()) == 1
+    c.check()
+    assert c.fork([0, 3], [1, 2]) == mp.MP_ERR_CAPACITY  # two partly filled pages; the list of copies is empty
+    c.check()
+    assert c.fork([0], [1]) == 0 and not c.m.free_pages()
+    c.check()
+
+
+# ---------------------------------------------------------- the sampled decode ----
+
+def test_prompt_into_the_contiguous_cache():
+    """A prompt's rows stored by the append into the cache of the sampled decode, as one page a sequence: hashed and
+    decoded like the same cache filled by hand, and like the paged decode over it."""
+    B, Hq, Hkv, cap, n = 2, 8, 2, 512, [300, 411]
+    q, k, v, cu = prompt_case(n, Hq, Hkv, seed=370)
+    out, lse = run_prompt(q, k, v, cu)
+    check_prompt(q, k, v, cu, out, lse)
+    kc, vc, by_hand, by_hand_v = (torch.zeros(B, Hkv, cap, D, dtype=torch.bfloat16, device="cuda") for _ in range(4))
+    lens, table = i32([0, 0]), i32([[0], [1]])
+    st = status_word()
+    mp.paged_append(mp.PagesShape(B, Hq, Hkv, D, B, cap, 1), k.cuda(), v.cuda(), table, lens, kc, vc, cu_new=i32(cu), status=st)
+    for b in range(B):
+        by_hand[b, :, :n[b]] = k[cu[b]:cu[b + 1]].transpose(0, 1).cuda()
+        by_hand_v[b, :, :n[b]] = v[cu[b]:cu[b + 1]].transpose(0, 1).cuda()
+    assert st.item() == 0 and lens.tolist() == n and torch.equal(kc, by_hand) and torch.equal(vc, by_hand_v)
+    W, q1 = rand(75 * 8, D, seed=380).cuda(), rand(B, Hq, D, seed=381)
+    k1, v1 = rand(B, Hkv, D, seed=382).cuda(), rand(B, Hkv, D, seed=383).cuda()
+
+    def decode(window, k_cache, v_cache):
+        shape, at = mp.Shape(B, Hq, Hkv, D, cap, 8, 75, 4, window), i32(n)
+        codes = torch.zeros(mp.codes_shape(shape)[1], dtype=torch.uint8, device="cuda")
+        mp.hash_keys(shape, k_cache, W, max(n), codes)
+        mp.append_token(shape, k1, v1, W, k_cache, v_cache, codes, at)
+        out, lse, ns = torch.zeros(B, Hq, D, device="cuda"), torch.zeros(B, Hq, device="cuda"), i32([[0] * Hq] * B)
+        ws = torch.empty(mp.decode_workspace_bytes(shape, max(n) + 1), dtype=torch.uint8, device="cuda")
+        mp.decode_attend(shape, q1.cuda(), W, codes, k_cache, v_cache, at, max(n) + 1, out, lse, ns, ws)
+        torch.cuda.synchronize()
+        return codes, at, out.cpu(), lse.cpu(), ns
+
+    for window in (64, cap):
+        a, b = decode(window, kc.clone(), vc.clone()), decode(window, by_hand.clone(), by_hand_v.clone())
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    mp.append_token(mp.Shape(B, Hq, Hkv, D, cap, 8, 75, 4, cap), k1, v1, W, kc, vc, a[0], lens)
+    got, got_lse = run_paged(q1, kc.cpu(), vc.cpu(), [[0], [1]], [x + 1 for x in n])
+    # the sampled decode with every token in its exact set; its own bars: 2e-3 relative L2, 1e-3 on lse
+    assert (got - a[2]).norm() / got.norm() <= 2e-3 and (got_lse - a[3]).abs().max() <= 1e-3
