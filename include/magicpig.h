@@ -352,8 +352,9 @@ typedef struct mp_prompt_shape {
  * a sequence a key that is not finite reaches the tokens that see it; the
  * values v must be finite: one that is not may also reach, in its dim,
  * up to 255 tokens before it.
- * A weight exp(.) is rounded to bf16 before it multiplies its v (relative
- * 2^-9, about the rounding of out itself); lse comes from the unrounded fp32.
+ * A weight exp(.) is rounded to bf16 before it multiplies its v (off by up to
+ * 2^-8 of itself, like the rounding of out); the sums that it is divided by, and
+ * lse, come from the unrounded fp32.
  * status also receives MP_ERR_CUDA if the kernel's internal pipeline stalled
  * (a bounded wait expired; out and lse are then incomplete).
  */

@@ -21,6 +21,14 @@ operations on them (``pages_reserve``, ``pages_fork``, ``pages_free``,
     paged_append(shape, k_new, v_new, table, lens, k_pages, v_pages)
     paged_attend(shape, q, k_pages, v_pages, table, lens, max_len, out, lse, workspace)
     pages_free(shape, ended, table, lens, refs)
+
+A prompt into the cache of the sampled decode, ``[batch, kv heads, capacity, d]``, which is one page of ``capacity``
+tokens a sequence (``n_pages=batch, page_size=capacity, max_pages=1`` and a table of 0, 1, ..)::
+
+    prompt_attend(prompt_shape, q, k, v, cu, out, lse)
+    paged_append(one_page_each, k, v, table, lens, k_cache, v_cache, cu_new=cu)
+    hash_keys(shape, k_cache, W, longest, codes)
+    append_token(...); decode_attend(...)                       # each step; paged_attend reads the same cache exactly
 """
 from ._binding import (  # noqa: F401
     MagicPIGError,

@@ -5,10 +5,12 @@
 // one pass over the unit's tokens with a running maximum and sum per head.
 // The floor is HBM: 512 bytes per (token, kv head), each read once; the
 // products are 2 d G multiply-adds on them, far below the tensor rate.  Measured
-// with 32 / 8 heads, 16 sequences of 32k to 131k tokens in pages of 16: 776 us
+// with 32 / 8 heads, 16 sequences of 32k to 131k tokens in pages of 16: 775 us
 // for 5.46 GB, 7.0 TB/s (a copy runs at 6.55); one sequence of 16k 19 us (floor
-// 10: launches, the first loads' latency and the join are the rest); 256 of up
-// to 300 37 us (floor 25), 47 with units' ends counted as nothing.
+// 10: launches, the first loads' latency and the join, whose grid of C - 1 blocks
+// a head of the group is 1180 for 32 results and finds no room beside the
+// attention's blocks, are the rest); 256 of up to 300 37 us (floor 25), 47 with
+// units' ends counted as nothing.
 //
 // Split: the 64-token blocks of all units, unit after unit, form one line of
 // W places (a unit's end takes kEndCost, as it costs about as much), and the C
@@ -27,7 +29,7 @@
 // in registers, and the warps meet only at the end of a unit.  mma.sync and
 // not tcgen05: 8 heads fill a 16-row tile of either poorly, and the tensor
 // pipe idles here anyway.  P enters its product as three bf16 parts (24 bits):
-// the result is fp32, and one bf16 part would cost 2^-9.
+// the result is fp32, and one bf16 part would be off by up to 2^-8 of a weight.
 #include <math.h>
 
 #include "mp_pages.cuh"

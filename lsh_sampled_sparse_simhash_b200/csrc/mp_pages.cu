@@ -12,11 +12,16 @@
 // The plans move a few hundred kilobytes at most and are bound by latency
 // (dependent loads and cluster barriers): ending 40 of 256 sequences and
 // reserving for the rest takes 15 us with 124k pages and 1000 columns, a
-// compaction plan of 2900 pages 9 us.  A cluster, and not more blocks, because
+// compaction plan of 2900 pages 9 us.  Past 131072 pages a warp's run no longer
+// fits its registers and the second walk reads the counts again, 32 at a time:
+// reserve 10.5 us at 131072 pages, 17 at 131073, 26 at 2^20; compact, half of
+// the pages in use and half of those to be moved, 41, 56 and 349 us.  A cluster,
+// and not more blocks, because
 // its barrier costs under a microsecond while a second launch costs two.  The
 // page copies and the append are bound by HBM: 88 MB in 13 us (6.7 TB/s), 196
-// MB of a strided projection's rows in 28.5 us (6.9 TB/s).  Loads of the counts bypass L1 (ld.global.cg): other blocks of the
-// cluster change them between two barriers.
+// MB of a strided projection's rows in 28.5 us (6.9 TB/s).  Loads of the counts
+// bypass L1 (ld.global.cg): other blocks of the cluster change them between two
+// barriers.
 #include <cooperative_groups.h>
 
 #include "mp_pages.cuh"

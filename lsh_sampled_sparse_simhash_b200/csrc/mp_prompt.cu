@@ -7,8 +7,8 @@
 // the tensor rate (2 x 128^3 multiply-adds a tile of 128 rows and 128 keys) and,
 // as closely, by the exponentials (128^2 a tile, 16 a cycle and SM): 1024
 // cycles each at the nominal rates.  Measured at 16384 tokens, 32 / 8 heads:
-// 1.87 ms, 1180 TFLOP/s of causal work (72% of the measured burst rate of a
-// library product, 89% of its rate under the power cap, which holds here too),
+// 1.85 ms, 1190 TFLOP/s of causal work (72% of the measured burst rate of a
+// library product, 90% of its rate under the power cap, which holds here too),
 // tensor pipe and special functions 64% busy each.
 //
 // An item is 2 kTok tokens of one sequence and one kv head: two 128-row query
@@ -391,7 +391,8 @@ __device__ __noinline__ Reference far_reference(Reference r, float top, int lim,
 // 2^(half a unit in the last place of m), which would leave fp32's range for
 // scores past 2^33.  So a reference beyond kFar is kept as the score itself
 // (`far`), and every score of the row is taken relative to it first.  Scores
-// are read twice from TMEM, through three buffers of 32: all 128 at once spill.
+// are read twice from TMEM, through three buffers of 32: all 128 at once spill
+// (three buffers do not for G = 1, 2 and 4; 4 bytes for 8, 32 for the others).
 __device__ __forceinline__ void row_tile(float &m, bool &far, uint64_t *l, int lim, bool masked, bool o_used, uint32_t s_col,
                                          uint32_t o_col, uint32_t p_bar, int lane)
 {
