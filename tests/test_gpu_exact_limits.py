@@ -119,6 +119,18 @@ def test_prompt_groups_of_sequences(hq, hkv, lens):
         check_prompt(q[at, h:h + 1], k[at, u:u + 1], v[at, u:u + 1], [0, max(lens)], out[at, h:h + 1], lse[at, h:h + 1])
 
 
+def test_prompt_many_heads():
+    """More heads than a group of sequences has room for tokens: 109 tokens a group, 300 kv heads of three query heads."""
+    lens = [130, 1, 0, 77, 20]
+    q, k, v, cu = prompt_case(lens, 900, 300, seed=325)
+    out, lse, status = attend_rows(q, k, v, cu)
+    assert status == 0 and (lse != 7.0).all()
+    for u in (0, 150, 299):
+        check_prompt(q[:, 3 * u:3 * u + 3], k[:, u:u + 1], v[:, u:u + 1], cu, out[:, 3 * u:3 * u + 3], lse[:, 3 * u:3 * u + 3])
+    one = [x[:130].contiguous() for x in (q, k, v)]
+    assert torch.equal(out[:130, 200:260], attend_rows(*one, [0, 130])[0][:, 200:260])
+
+
 @pytest.mark.parametrize("threads", [1, 8])
 def test_first_calls_of_threads(threads):
     """A process whose first call comes from a new host thread, or from eight at once."""
@@ -164,6 +176,19 @@ def test_paged_reports_every_bad_page(size, bad):
     table[0][1] = bad
     out, lse = run_paged(q, k, v, table, lens, want=mp.MP_ERR_CAPACITY)
     check_paged(q, k, v, table, lens, out, lse)
+
+
+@pytest.mark.parametrize("batch,hkv", [(4096, 2), (4095, 16)])
+def test_paged_largest_batches(batch, hkv):
+    """As many sequences as a call takes, and as many (sequence, kv head) pairs; empty ones and a long one among them."""
+    r = random.Random(batch)
+    lens = [r.choice((0, 0, 1, 3, 17, 40)) for _ in range(batch)]
+    lens[batch // 3] = 700
+    q, k, v, table = paged_case(lens, hkv, hkv, 16, seed=345)
+    out, lse = run_paged(q, k, v, table, lens)
+    some = sorted(r.sample(range(batch), 60) + [0, batch // 3, batch - 1])
+    check_paged(q[some], k, v, [table[b] for b in some], [lens[b] for b in some], out[some], lse[some])
+    assert (out != 7.0).all() and (lse != 7.0).all() and torch.equal(torch.isfinite(lse[:, 0]), torch.tensor(lens) > 0)
 
 
 def test_append_one_row_of_every_sequence():
@@ -249,6 +274,18 @@ def test_fork_with_too_few_pages_changes_nothing():
     assert c.fork([0, 3], [1, 2]) == mp.MP_ERR_CAPACITY  # two partly filled pages; the list of copies is empty
     c.check()
     assert c.fork([0], [1]) == 0 and not c.m.free_pages()
+    c.check()
+
+
+def test_fork_of_empty_and_reserved_sequences():
+    """A source without tokens gives one without; pages that a source holds past its length stay its own."""
+    c = Cache(6, 20, 4, 5)
+    assert c.reserve([8, 13, 0, 0, 0, 0])
+    c.append([8, 2, 0, 0, 0, 0])
+    assert c.fork([0, 1, 2], [3, 4, 5]) == 0
+    c.check()
+    assert c.reserve([1] * 6)
+    c.append([1] * 6)
     c.check()
 
 
